@@ -347,7 +347,7 @@ def _rope(st):
 
 
 def _append_plain(q, scale, x, start, n, begin, rows, c):
-    """The touched blocks as values after the append: [B][H][rows][D], in the type of the rows."""
+    """The touched blocks as values after the append: [B][rows][H][D], in the type of the rows."""
     B, H, cap, D = q.shape
     bl, T = c["block"], c["tokens"]
     at = begin[:, None].long() + torch.arange(rows, device="cuda")           # [B][rows]
@@ -364,7 +364,7 @@ def _append_plain(q, scale, x, start, n, begin, rows, c):
     blocks = val.view(B, H, rows // bl, bl, D)
     need = _block_scale(torch.where(is_new[:, None, :, None], new, 0.0).view_as(blocks).abs().amax((3, 4)), c["fmt"])
     s = torch.maximum(need, s_old.view(B, H, rows // bl, bl).amax(3))[..., None, None]
-    return (_to8(blocks, s, c["fmt"]).float() * s).view(B, H, rows, D).to(x.dtype)
+    return (_to8(blocks, s, c["fmt"]).float() * s).view(B, H, rows, D).transpose(1, 2).to(x.dtype).contiguous()
 
 
 def _append(st):
@@ -510,7 +510,7 @@ def exact(c, seed):
                     s[:, 0] = torch.maximum(s[:, 0], first)
                 s = s.repeat_interleave(bl, 1)[..., None]
                 out[b, :, :end - b0] = grid(val / s.clamp(min=2.0 ** -140)) * s
-            return out
+            return out.transpose(1, 2).contiguous()
         return one(st["k"], st["ks"], st["K"]), one(st["v"], st["vs"], st["V"]), None
     if c["op"] == "evict":
         return None
