@@ -76,6 +76,7 @@ typedef enum { MSA_F32 = 0, MSA_BF16 = 1 } msa_dtype;
 #define MSA_DEVERR_BAD_DOC_ID 0x1u      /* an id outside [0, n_docs) reached attention */
 #define MSA_DEVERR_CACHE_OVERFLOW 0x2u  /* cache_len + tokens > cache_capacity */
 #define MSA_DEVERR_WAIT_TIMEOUT 0x4u    /* a pipeline barrier wait ran out */
+#define MSA_DEVERR_BAD_LENGTH 0x8u      /* a cache length or token count out of range (msa_cache8_*) */
 
 /*
  * The memory's shape.  Documents [Evermind sec. 2: the corpus is split into
@@ -490,6 +491,195 @@ MSA_API msa_status msa_sparse_attend_backward(const msa_memory *mem, const void 
                                               int32_t pos_offset, const void *dO, float *dQ,
                                               float *d_cache_k, float *d_cache_v,
                                               float *d_content, msa_stream stream);
+
+/*
+ * Rotary positions for the attention calls that take Q and K already rotated
+ * (msa_cache8_append, msa_cache8_attend): head layouts and long-context
+ * scalings that the fixed rotation inside msa_sparse_attend does not have.
+ * The first `rotary_dim` elements of every head are rotated in pairs, pair i
+ * by the angle position * freq_i, and multiplied by `magnitude`; the rest of
+ * the head is copied:
+ *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin)
+ *   layout : MSA_ROPE_HALF pairs element i with i + rotary_dim / 2,
+ *            MSA_ROPE_INTERLEAVED pairs 2 i with 2 i + 1
+ *   freq_i = theta^(-2 i / rotary_dim), scaled by
+ *     MSA_ROPE_LINEAR : freq_i / factor (position interpolation)
+ *     MSA_ROPE_NTK    : theta * factor^(r / (r - 2)) in place of theta, r = rotary_dim
+ *     MSA_ROPE_YARN   : freq_i / factor where the pair turns less than once within
+ *                       original_length, freq_i where it turns more than 32 times, a
+ *                       linear ramp over the pair index between them
+ *   factor : >= 1 (not read without a scaling); original_length: >= 1 for YARN
+ *   magnitude : 0 takes the scaling's own, 0.1 ln(factor) + 1 for YARN and 1 otherwise
+ * head_dim 2..512 and rotary_dim 2..head_dim, both even (NTK: rotary_dim > 2).
+ * Frequencies are kept as 64-bit fractions of a turn, so an angle is exact
+ * modulo one turn at every int64 position (negative ones too).  The handle is
+ * immutable and belongs to the device that was current at its creation.
+ */
+typedef enum { MSA_ROPE_HALF = 0, MSA_ROPE_INTERLEAVED = 1 } msa_rope_layout;
+typedef enum {
+  MSA_ROPE_NONE = 0,
+  MSA_ROPE_LINEAR = 1,
+  MSA_ROPE_NTK = 2,
+  MSA_ROPE_YARN = 3,
+} msa_rope_scaling;
+
+typedef struct {
+  int32_t head_dim;
+  int32_t rotary_dim;
+  double theta;
+  int32_t layout;          /* msa_rope_layout */
+  int32_t scaling;         /* msa_rope_scaling */
+  double factor;
+  int64_t original_length;
+  double magnitude;
+} msa_rope_config;
+
+typedef struct msa_rope msa_rope;
+
+MSA_API msa_status msa_rope_create(const msa_rope_config *cfg, msa_rope **out);
+MSA_API msa_status msa_rope_destroy(msa_rope *rope);
+
+/*
+ * Rotate the heads of `tokens` tokens, Q and K in one launch.
+ *   positions : device [tokens] int64
+ *   inverse   : 0 rotates; 1 applies the transpose (rotation by -angle, same
+ *               magnitude), which is the backward pass: gradients of the
+ *               outputs in, gradients of the inputs out
+ *   q, q_out  : device, token t's heads [q_heads][head_dim] dense at
+ *               q + t * q_stride (elements), so a slice of a joint projection
+ *               is read as it lies; likewise k (k_heads may be 0, k then NULL)
+ * An output may be its own input (same pointer and stride) and otherwise must
+ * not overlap an input.  Pointers need only element alignment (16-byte
+ * aligned rows run faster).  tokens may be 0.
+ */
+MSA_API msa_status msa_rope_apply(const msa_rope *rope, msa_dtype dtype, int64_t tokens,
+                                  const int64_t *positions, int32_t inverse, const void *q,
+                                  int32_t q_heads, int64_t q_stride, void *q_out,
+                                  int64_t q_out_stride, const void *k, int32_t k_heads,
+                                  int64_t k_stride, void *k_out, int64_t k_out_stride,
+                                  msa_stream stream);
+
+/*
+ * 8-bit local cache: the local K/V of a decode batch in one byte an element
+ * with one fp32 scale for each block of tokens and kv head.
+ *   k, v             : device [batch][H_kv][capacity][D], int8 or e4m3; an
+ *                      element stands for its value * the scale of its block
+ *   k_scale, v_scale : device fp32 [batch][H_kv][capacity / block_len]
+ *   cache_len        : device int32 [batch], rows held
+ *   weights          : device fp32 [batch][H_kv][capacity] or NULL: attention
+ *                      weight accumulated by each cached row
+ * A scale is the smallest power of two s with max|x| <= qmax * s over the
+ * block's rows (qmax 127 for int8, 448 for e4m3; 0 when every row is zero), so
+ * dividing and multiplying by it are exact and the one rounding is to the
+ * format, to nearest even.  A partly filled block whose new row needs a larger
+ * scale has its earlier rows rounded again at the new scale; scales at least
+ * double each time, so all roundings of an element together stay within one
+ * step of the final scale (int8).  A bf16 element holds any cached value exactly.
+ * block_len: 16, 32, 64 or 128; capacity a multiple of it.  H_kv, D and the
+ * element type of what goes in and out are the memory's.  All buffers are the
+ * caller's, 16-byte aligned.
+ */
+typedef enum { MSA_CACHE_INT8 = 0, MSA_CACHE_E4M3 = 1 } msa_cache8_format;
+
+typedef struct {
+  int32_t batch;
+  int32_t capacity;
+  int32_t block_len;
+  int32_t format; /* msa_cache8_format */
+  void *k;
+  void *v;
+  float *k_scale;
+  float *v_scale;
+  int32_t *cache_len;
+  float *weights;
+} msa_cache8;
+
+/*
+ * Append each query's new rows (K already rotated, see msa_rope_apply).
+ *   K, V     : device [batch][tokens][H_kv][D] in the memory's dtype, H_kv and
+ *              D dense; batch and token strides in elements, multiples of 16 bytes
+ *   n_tokens : device int32 [batch] or NULL: the first n_tokens[b] of the
+ *              query's tokens are appended, the rest is padding (NULL: all)
+ *   start    : device int32 [batch] or NULL: the row the first token goes to;
+ *              NULL appends at cache_len[b].  A start below cache_len drops the
+ *              rows from there on (rejected draft tokens).  A block that start
+ *              lies in keeps its scale unless start is its first row.
+ * cache_len[b] becomes start + n_tokens; weights of appended rows become 0.  Rows that
+ * pass the capacity are skipped and flagged (MSA_DEVERR_CACHE_OVERFLOW); a
+ * start or count out of range leaves the query as it was
+ * (MSA_DEVERR_BAD_LENGTH).  NaN is stored as 0 and an infinity as the largest
+ * value of the block's scale; neither enters the scale.
+ */
+MSA_API msa_status msa_cache8_append(const msa_memory *mem, const msa_cache8 *cache,
+                                     const void *K, const void *V, int32_t tokens,
+                                     int64_t k_batch_stride, int64_t k_token_stride,
+                                     int64_t v_batch_stride, int64_t v_token_stride,
+                                     const int32_t *n_tokens, const int32_t *start,
+                                     msa_stream stream);
+
+/*
+ * Values of the rows begin[b] .. begin[b] + rows - 1 (begin NULL: from row 0)
+ * in the memory's dtype, token-major like the framework's own local cache:
+ * K_out, V_out device [batch][rows][H_kv][D].  Rows outside [0, cache_len[b])
+ * read as zero.
+ */
+MSA_API msa_status msa_cache8_read(const msa_memory *mem, const msa_cache8 *cache,
+                                   const int32_t *begin, int32_t rows, void *K_out, void *V_out,
+                                   msa_stream stream);
+
+/* Scratch bytes msa_cache8_attend needs. */
+MSA_API size_t msa_cache8_attend_workspace_size(const msa_memory *mem, const msa_cache8 *cache,
+                                                int32_t tokens, int32_t k, int32_t n_q_heads);
+
+/*
+ * msa_sparse_attend over the 8-bit cache.  The query's last n_tokens[b] cached
+ * rows are its new tokens (msa_cache8_append ran before); token t attends over
+ *   [pooled K/V of every chunk of ids[b,0..k-1], all visible]
+ *   ++ [cached rows 0 .. cache_len[b] - n_tokens[b] + t]
+ * softmax scale 1/sqrt(D), query head h reading kv head h / (n_q_heads / H_kv).
+ *   Q, O     : device [batch][tokens][n_q_heads][D], Q already rotated
+ *   n_tokens : device int32 [batch] or NULL (all); O and lse of padding tokens
+ *              are left as they were
+ *   lse      : device fp32 [batch][tokens][n_q_heads] or NULL: the natural log
+ *              of the softmax's sum; a token that sees nothing has O = 0 and
+ *              lse = -inf
+ *   weight_decay : negative leaves cache->weights alone; otherwise, for every
+ *              cached row j, weights[b][g][j] = weight_decay * weights[b][g][j]
+ *              + the softmax weight row j received from this call's tokens and
+ *              the heads of kv head g (0 overwrites; rows beyond cache_len stay)
+ * k may be 0 (content and ids are then not read).  A group
+ * (n_q_heads / H_kv) is at most 16.  A count out of [0, tokens] or a length
+ * outside [0, capacity] counts as no tokens (MSA_DEVERR_BAD_LENGTH).
+ */
+MSA_API msa_status msa_cache8_attend(const msa_memory *mem, const void *content,
+                                     const int32_t *ids, int32_t k, const msa_cache8 *cache,
+                                     int32_t tokens, int32_t n_q_heads, const void *Q,
+                                     const int32_t *n_tokens, void *O, float *lse,
+                                     float weight_decay, void *workspace,
+                                     size_t workspace_bytes, msa_stream stream);
+
+/* Scratch bytes msa_cache8_evict needs. */
+MSA_API size_t msa_cache8_evict_workspace_size(const msa_memory *mem, const msa_cache8 *cache);
+
+/*
+ * Eviction by accumulated attention weight.  A query of `cache` (with weights)
+ * that holds more than `budget` rows keeps, for each kv head by itself, its
+ * last partial block, its last ceil(recent / block_len) full blocks and of the
+ * other full blocks those with the largest summed weight (ties: the lower
+ * block; a NaN sum counts as nothing), (budget - partial) / block_len full
+ * blocks in all; the kept rows move together in their order, with their scales
+ * and weights, and cache_len shrinks.  Blocks move as they are: nothing is
+ * rounded again.  Shorter queries keep every row.
+ *   out : the cache that receives the rows; the same struct contents (in
+ *         place), or a cache of the same batch, format and block_len whose
+ *         buffers do not overlap and whose capacity is >= min(capacity,
+ *         budget); it needs weights too.  Its weights of rows that the query
+ *         no longer holds become 0; its other bytes there stay.
+ *   budget >= block_len; 0 <= recent <= budget
+ */
+MSA_API msa_status msa_cache8_evict(const msa_memory *mem, const msa_cache8 *cache,
+                                    const msa_cache8 *out, int32_t budget, int32_t recent,
+                                    void *workspace, size_t workspace_bytes, msa_stream stream);
 
 /* Read and clear the device error word of the current device (synchronises/* Read and clear the device error word of the current device (synchronises/* Read and clear the device error word of the current device (synchronises
  * `stream`).  *bits receives the MSA_DEVERR_* bits; returns MSA_ERR_TIMEOUT or

@@ -108,3 +108,31 @@ def test_adaptive_interleave_validates_before_touching_the_gpu():
     assert b"null" in lib.msa_last_error()
     assert lib.msa_interleave(None, None, None, 1, 1, 1, 1, None, None, None, None, None, 0,
                               None) == 1
+
+
+def test_rope_create_rejects_bad_configs_without_a_gpu():
+    lib = msa.lib()
+    base = dict(head_dim=64, rotary_dim=64, theta=1e4, layout=0, scaling=0, factor=1.0,
+                original_length=0, magnitude=0.0)
+    for kw, status in ((dict(head_dim=0), 2), (dict(head_dim=514), 2), (dict(head_dim=63), 2),
+                       (dict(rotary_dim=66), 1), (dict(rotary_dim=3), 1), (dict(theta=1.0), 1),
+                       (dict(theta=float("nan")), 1), (dict(layout=2), 1), (dict(scaling=4), 1),
+                       (dict(scaling=1, factor=0.5), 1), (dict(scaling=2, factor=2.0, rotary_dim=2), 1),
+                       (dict(scaling=3, factor=2.0), 1), (dict(magnitude=float("inf")), 1)):
+        cfg, h = msa.RopeConfig(**{**base, **kw}), ctypes.c_void_p()
+        assert lib.msa_rope_create(ctypes.byref(cfg), ctypes.byref(h)) == status, kw
+        assert not h.value and lib.msa_last_error()
+
+
+def test_serving_calls_reject_null_handles():
+    lib = msa.lib()
+    assert lib.msa_rope_create(None, None) == 1
+    assert lib.msa_rope_destroy(None) == 1
+    assert lib.msa_rope_apply(None, 0, 1, None, 0, None, 1, 64, None, 64, None, 0, 0, None, 0, None) == 1
+    assert lib.msa_cache8_append(None, None, None, None, 1, 0, 0, 0, 0, None, None, None) == 1
+    assert lib.msa_cache8_read(None, None, None, 1, None, None, None) == 1
+    assert lib.msa_cache8_attend_workspace_size(None, None, 1, 1, 1) == 0
+    assert lib.msa_cache8_attend(None, None, None, 0, None, 1, 1, None, None, None, None, -1.0, None,
+                                 0, None) == 1
+    assert lib.msa_cache8_evict_workspace_size(None, None) == 0
+    assert lib.msa_cache8_evict(None, None, None, 64, 0, None, 0, None) == 1

@@ -1,0 +1,516 @@
+// cache8.cuh -- the 8-bit local cache: append (quantise), read (dequantise)
+// and eviction by accumulated attention weight.
+//
+// A block of block_len rows of one (query, kv head) shares one scale, the
+// smallest power of two s with max|x| <= qmax * s.  Powers of two make x / s
+// and q * s exact in fp32, so the only rounding is the one to the format; a
+// block whose scale grows rounds its earlier rows again at steps that at least
+// double, so the roundings of an element sum to at most one final step.  An
+// amax / qmax scale would halve the step at best, but let every small growth
+// add half a step to every earlier row.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace msa {
+
+// ---------------------------------------------------------------- formats
+template <int FMT> struct Fmt8;
+
+template <> struct Fmt8<MSA_CACHE_INT8> {
+  static constexpr float kMax = 127.0f;
+  // four values, each already divided by the scale -> four bytes
+  static __device__ __forceinline__ uint32_t pack4(const float v[4]) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w |= (static_cast<uint32_t>(__float2int_rn(v[i])) & 0xffu) << (8 * i);
+    return w;
+  }
+  static __device__ __forceinline__ void unpack4(uint32_t w, float v[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * i)));
+  }
+};
+
+template <> struct Fmt8<MSA_CACHE_E4M3> {
+  static constexpr float kMax = 448.0f;
+  static __device__ __forceinline__ uint32_t pack4(const float v[4]) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+  }
+  static __device__ __forceinline__ void unpack4(uint32_t w, float v[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+          static_cast<__nv_fp8x2_storage_t>(w >> (16 * i)), __NV_E4M3);
+      const float2 f = __half22float2(__half2(h));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
+
+// The smallest power of two s with amax <= kMax * s (at least 2^-126, so that
+// 1 / s is finite); 0 for amax = 0.  amax is finite.
+template <int FMT>
+__device__ __forceinline__ float block_scale(float amax) {
+  if (amax == 0.0f) return 0.0f;
+  int e;
+  const float m = frexpf(amax, &e);  // amax = m 2^e, m in [0.5, 1)
+  constexpr int eq = FMT == MSA_CACHE_INT8 ? 7 : 9;
+  constexpr float mq = Fmt8<FMT>::kMax / static_cast<float>(1 << eq);  // kMax = mq 2^eq
+  return ldexpf(1.0f, max(e - eq + (m > mq ? 1 : 0), -126));
+}
+
+// What is stored of a value: NaN as 0, an infinity as the block's largest value.
+template <int FMT>
+__device__ __forceinline__ float to_grid(float x, float inv) {
+  if (!isfinite(x)) return x != x ? 0.0f : copysignf(Fmt8<FMT>::kMax, x);
+  return x * inv;
+}
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.0f;
+}
+
+// 16 consecutive elements of T as floats (64 or 32 bytes, 16-byte aligned)
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, float v[16]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load4(p + 4 * i, v + 4 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(p + 8 * i);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store16(T *p, const float v[16]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store4(p + 4 * i, v + 4 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint4 x;
+      x.x = pack_bf16x2(v[8 * i], v[8 * i + 1]);
+      x.y = pack_bf16x2(v[8 * i + 2], v[8 * i + 3]);
+      x.z = pack_bf16x2(v[8 * i + 4], v[8 * i + 5]);
+      x.w = pack_bf16x2(v[8 * i + 6], v[8 * i + 7]);
+      *reinterpret_cast<uint4 *>(p + 8 * i) = x;
+    }
+  }
+}
+template <int FMT>
+__device__ __forceinline__ uint4 pack16(const float v[16], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = to_grid<FMT>(v[4 * i + j], inv);
+    w[i] = Fmt8<FMT>::pack4(y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int FMT>
+__device__ __forceinline__ void unpack16(uint4 x, float s, float v[16]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    Fmt8<FMT>::unpack4(w[i], v + 4 * i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[4 * i + j] *= s;
+  }
+}
+
+// The rows a call appends to query b: start, count; false (and flagged by
+// `report`) when they are out of range.
+struct AppendRange {
+  int start, count;
+};
+__device__ __forceinline__ bool append_range(const int32_t *start, const int32_t *cache_len,
+                                             const int32_t *n_tokens, int b, int tokens, int cap,
+                                             bool report, AppendRange &r) {
+  r.start = start ? start[b] : cache_len[b];
+  r.count = n_tokens ? n_tokens[b] : tokens;
+  const bool ok = r.start >= 0 && r.start <= cap && r.count >= 0 && r.count <= tokens;
+  if (report && !ok) raise_device_error(MSA_DEVERR_BAD_LENGTH);
+  if (report && ok && r.count > cap - r.start) raise_device_error(MSA_DEVERR_CACHE_OVERFLOW);
+  return ok;
+}
+
+__device__ __forceinline__ int append_end(const AppendRange &r, int cap) {
+  return r.count > cap - r.start ? cap : r.start + r.count;
+}
+
+// ---------------------------------------------------------------- append
+struct AppendArgs {
+  const void *K, *V;
+  int64_t kb, kt, vb, vt;  // batch and token strides, elements
+  int tokens, H_kv, cap, bl;
+  uint8_t *k8, *v8;
+  float *ks, *vs;
+  int32_t *cache_len;
+  const int32_t *n_tokens, *start;
+  float *weights;
+};
+
+// grid (2 * H_kv, blocks a query can touch, B), block 256: one CTA quantises the new rows of one
+// block of one head of K or V.  A task is 16 elements of a row, NT tasks a thread, so the block's
+// new rows stay in registers between the maximum and the rounding.  set_len: write the new
+// cache_len here (start given: no CTA reads cache_len).
+template <typename T, int D, int FMT, int NT>
+__global__ void __launch_bounds__(256)
+cache8_append_kernel(AppendArgs a, int set_len) {
+  constexpr int CPR = D / 16;
+  __shared__ float red[8];
+  griddep_wait();
+  griddep_launch();
+  const int h = blockIdx.x >> 1, which = blockIdx.x & 1, b = blockIdx.z;
+  const bool first = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+  AppendRange r;
+  if (!append_range(a.start, a.cache_len, a.n_tokens, b, a.tokens, a.cap, first, r)) return;
+  const int end = append_end(r, a.cap);
+  if (first && set_len) a.cache_len[b] = end;
+  const int blk = r.start / a.bl + blockIdx.y;
+  const int x0 = blk * a.bl;  // first row of the block
+  if (x0 >= end) return;
+  const int lo = max(x0, r.start), hi = min(x0 + a.bl, end);  // new rows [lo, hi)
+  const T *src = static_cast<const T *>(which ? a.V : a.K) + b * (which ? a.vb : a.kb) +
+                 static_cast<int64_t>(h) * D;
+  const int64_t ts = which ? a.vt : a.kt;
+  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + h;
+  uint8_t *dst = (which ? a.v8 : a.k8) + (bh * a.cap + x0) * D;
+  float *scale = (which ? a.vs : a.ks) + bh * (a.cap / a.bl) + blk;
+  float v[NT][16];
+  float amax = 0.0f;
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const int task = threadIdx.x + 256 * u, row = x0 + task / CPR;
+    if (row >= lo && row < hi) {
+      load16(src + (row - r.start) * ts + (task % CPR) * 16, v[u]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(v[u][i]));
+    }
+  }
+  amax = warp_max(amax);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) amax = fmaxf(amax, red[w]);
+  const float s_old = lo > x0 ? *scale : 0.0f;
+  const float s = fmaxf(block_scale<FMT>(amax), s_old);
+  const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+  __syncthreads();  // every thread has read the old scale
+  if (threadIdx.x == 0 && (s != s_old || lo == x0)) *scale = s;
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const int task = threadIdx.x + 256 * u, row = x0 + task / CPR;
+    uint4 *p = reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(task) * 16);
+    if (row >= lo && row < hi) {
+      *p = pack16<FMT>(v[u], inv);
+    } else if (row < lo && s > s_old) {  // earlier rows of a block whose scale grew
+      float old[16];
+      unpack16<FMT>(*p, s_old, old);
+      *p = pack16<FMT>(old, inv);
+    }
+  }
+  if (a.weights && which == 0)
+    for (int x = lo + threadIdx.x; x < hi; x += 256) a.weights[bh * a.cap + x] = 0.0f;
+}
+
+// cache_len after an append at cache_len (start NULL): every CTA of the append has read it.
+__global__ void cache8_advance_kernel(int32_t *__restrict__ cache_len,
+                                      const int32_t *__restrict__ n_tokens, int B, int tokens,
+                                      int cap) {
+  griddep_wait();
+  griddep_launch();
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b >= B) return;
+  AppendRange r;
+  if (append_range(nullptr, cache_len, n_tokens, b, tokens, cap, false, r))
+    cache_len[b] = append_end(r, cap);
+}
+
+// ---------------------------------------------------------------- read
+// grid (ceil(rows * H_kv * D / 16 / 256), 2, B): 16 elements a thread, token-major out.
+template <typename T, int D, int FMT>
+__global__ void __launch_bounds__(256)
+cache8_read_kernel(const uint8_t *__restrict__ k8, const uint8_t *__restrict__ v8,
+                   const float *__restrict__ ks, const float *__restrict__ vs,
+                   const int32_t *__restrict__ cache_len, const int32_t *__restrict__ begin,
+                   int rows, int H_kv, int cap, int bl, T *__restrict__ K, T *__restrict__ V) {
+  constexpr int CPR = D / 16;
+  griddep_wait();
+  griddep_launch();
+  const int b = blockIdx.z;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= static_cast<int64_t>(rows) * H_kv * CPR) return;
+  const int c = static_cast<int>(i % CPR), h = static_cast<int>(i / CPR % H_kv);
+  const int x = static_cast<int>(i / CPR / H_kv);
+  const int64_t row = static_cast<int64_t>(begin ? begin[b] : 0) + x;
+  const int len = min(cache_len[b], cap);
+  float v[16];
+  if (row >= 0 && row < len) {
+    const int64_t bh = static_cast<int64_t>(b) * H_kv + h;
+    const uint8_t *src = (blockIdx.y ? v8 : k8) + (bh * cap + row) * D + c * 16;
+    const float s = (blockIdx.y ? vs : ks)[bh * (cap / bl) + row / bl];
+    unpack16<FMT>(*reinterpret_cast<const uint4 *>(src), s, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+  }
+  store16((blockIdx.y ? V : K) + (static_cast<int64_t>(b) * rows * H_kv * CPR + i) * 16, v);
+}
+
+// ---------------------------------------------------------------- evict
+constexpr int kSelThreads = 512;
+
+// An order-preserving key of a block's summed weight; a NaN is the lowest.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// What an eviction keeps of one query: full blocks, recent ones among them, new length.
+struct EvictPlan {
+  int len, full, tail, keep, recent, new_len;
+};
+__device__ __forceinline__ EvictPlan evict_plan(int len, int cap, int bl, int budget, int recent) {
+  EvictPlan p;
+  p.len = max(0, min(len, cap));
+  p.full = p.len / bl;
+  p.tail = p.len % bl;
+  p.keep = p.len > budget ? (budget - p.tail) / bl : p.full;
+  p.recent = min((recent + bl - 1) / bl, p.keep);
+  p.new_len = p.keep * bl + p.tail;
+  return p;
+}
+
+// Exclusive prefix count of `flag` over the CTA's threads; *total gets the sum.
+__device__ __forceinline__ int cta_prefix(bool flag, int *warp_sums, int *total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const unsigned m = __ballot_sync(0xffffffffu, flag);
+  if (lane == 0) warp_sums[warp] = __popc(m);
+  __syncthreads();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) {
+    const int n = warp_sums[w];
+    before += w < warp ? n : 0;
+    sum += n;
+  }
+  __syncthreads();
+  *total = sum;
+  return before + __popc(m & ((1u << lane) - 1));
+}
+
+// grid (B * H_kv), block kSelThreads: which blocks stay, in order -> src_block[bh][0 .. keep).
+// A block's weight is summed in 64 bits and compared in 32, so the choice does not hang on the
+// order of the sum.  The keep - recent heaviest of the older blocks: a radix select over the keys
+// (four passes of 8 bits) finds the smallest kept key, then one pass in block order keeps all
+// larger keys and the first of the equal ones.
+__global__ void __launch_bounds__(kSelThreads)
+cache8_select_kernel(const float *__restrict__ weights, const int32_t *__restrict__ cache_len,
+                     int H_kv, int cap, int bl, int budget, int recent,
+                     uint32_t *__restrict__ keys, int32_t *__restrict__ src_block,
+                     int32_t *__restrict__ lens) {
+  __shared__ int hist[256];
+  __shared__ int warp_sums[kSelThreads / 32];
+  __shared__ int digit, above;
+  griddep_wait();
+  griddep_launch();
+  const int64_t bh = blockIdx.x;
+  const int b = blockIdx.x / H_kv, nb = cap / bl;
+  const EvictPlan p = evict_plan(cache_len[b], cap, bl, budget, recent);
+  if (blockIdx.x % H_kv == 0 && threadIdx.x == 0) {
+    lens[2 * b] = p.len;
+    lens[2 * b + 1] = p.new_len;
+  }
+  int32_t *src = src_block + bh * (nb + 1);
+  uint32_t *key = keys + bh * nb;
+  const int old = p.full - p.recent;     // blocks that compete
+  const int want = p.keep - p.recent;    // of which these stay
+  if (threadIdx.x == 0 && p.tail > 0) src[p.keep] = p.full;
+  for (int j = threadIdx.x; j < p.recent; j += kSelThreads) src[want + j] = old + j;
+  if (want == old) {
+    for (int j = threadIdx.x; j < old; j += kSelThreads) src[j] = j;
+    return;
+  }
+  const float *w = weights + bh * cap;
+  for (int j = threadIdx.x; j < old; j += kSelThreads) {
+    double s = 0.0;
+    const float4 *row = reinterpret_cast<const float4 *>(w + static_cast<int64_t>(j) * bl);
+    for (int i = 0; i < bl / 4; ++i) {
+      const float4 x = row[i];
+      s += static_cast<double>(x.x);
+      s += static_cast<double>(x.y);
+      s += static_cast<double>(x.z);
+      s += static_cast<double>(x.w);
+    }
+    key[j] = weight_key(static_cast<float>(s));
+  }
+  if (want == 0) return;
+  uint32_t prefix = 0, mask = 0;
+  int left = want;  // the left-th largest key among those that match the prefix
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int j = threadIdx.x; j < old; j += kSelThreads)
+      if ((key[j] & mask) == prefix) atomicAdd(&hist[(key[j] >> shift) & 255], 1);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int n = 0, d = 255;
+      for (; d > 0; --d) {
+        if (n + hist[d] >= left) break;
+        n += hist[d];
+      }
+      digit = d;
+      above = n;
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(digit) << shift;
+    mask |= 255u << shift;
+    left -= above;
+  }
+  // `prefix` is the smallest kept key, `left` of the blocks that have it stay (the first ones)
+  int kept = 0, equal = 0;
+  for (int j0 = 0; j0 < old; j0 += kSelThreads) {
+    const int j = j0 + threadIdx.x;
+    const uint32_t x = j < old ? key[j] : 0u;
+    int n;
+    const bool eq = j < old && x == prefix;
+    const int e = equal + cta_prefix(eq, warp_sums, &n);
+    equal += n;
+    const bool keep = j < old && (x > prefix || (eq && e < left));
+    const int d = kept + cta_prefix(keep, warp_sums, &n);
+    kept += n;
+    if (keep) src[d] = j;
+  }
+}
+
+struct EvictMove {
+  const uint8_t *k8, *v8;
+  const float *ks, *vs, *w;
+  uint8_t *ok8, *ov8;
+  float *oks, *ovs, *ow;
+  int32_t *out_len;
+  int H_kv, cap, out_cap, bl, D;
+};
+
+// grid (ceil(streams / 128), B * H_kv, parts), block 128.  Blocks move as units, so every piece of
+// a block (16 bytes of K, V or the weights, one scale) is a stream of its own along the kept
+// blocks, owned by one thread.  Destinations never lie behind their sources and a thread loads a
+// wave before it stores it, so in place (one part) needs no synchronisation at all: a wave's
+// stores reach only blocks at or below sources that the same thread has loaded.  Into another
+// cache the kept blocks are split over `parts`.
+constexpr int kMoveWave = 16;
+__global__ void __launch_bounds__(128)
+cache8_move_kernel(EvictMove m, const int32_t *__restrict__ src_block,
+                   const int32_t *__restrict__ lens, int in_place) {
+  griddep_wait();
+  griddep_launch();
+  const int64_t bh = blockIdx.y;
+  const int b = blockIdx.y / m.H_kv, nb = m.cap / m.bl;
+  const int len = lens[2 * b], new_len = lens[2 * b + 1];
+  const int32_t *src = src_block + bh * (nb + 1);
+  const int pieces = m.bl * m.D / 16, wp = m.bl / 4;
+  const int s = blockIdx.x * 128 + threadIdx.x;
+  if (s == 0 && blockIdx.y % m.H_kv == 0 && blockIdx.z == 0) m.out_len[b] = new_len;
+  // weights of rows no longer held (the out-of-place cache's own, up to its capacity)
+  const int live = (new_len + m.bl - 1) / m.bl;  // blocks written
+  const int per = (live + gridDim.z - 1) / gridDim.z;
+  const int j0 = blockIdx.z * per, j1 = min(live, j0 + per);
+  const int tail = new_len % m.bl;
+  if (s >= 2 * pieces + wp + 2) return;
+  if (s < 2 * pieces + wp) {
+    const uint8_t *in;
+    uint8_t *out;
+    int64_t block_bytes;
+    int piece, row;
+    if (s < 2 * pieces) {
+      const bool v = s >= pieces;
+      piece = v ? s - pieces : s;
+      row = piece * 16 / m.D;
+      block_bytes = static_cast<int64_t>(m.bl) * m.D;
+      in = (v ? m.v8 : m.k8) + bh * m.cap * m.D;
+      out = (v ? m.ov8 : m.ok8) + bh * m.out_cap * m.D;
+    } else {
+      piece = s - 2 * pieces;
+      row = piece * 4;
+      block_bytes = static_cast<int64_t>(m.bl) * 4;
+      in = reinterpret_cast<const uint8_t *>(m.w + bh * m.cap);
+      out = reinterpret_cast<uint8_t *>(m.ow + bh * m.out_cap);
+    }
+    const bool is_w = s >= 2 * pieces;
+    in += piece * 16;
+    out += piece * 16;
+    for (int j = j0; j < j1; j += kMoveWave) {
+      uint4 x[kMoveWave];
+      bool go[kMoveWave];
+#pragma unroll
+      for (int u = 0; u < kMoveWave; ++u) {
+        go[u] = false;
+        if (j + u < j1) {
+          const int from = src[j + u];
+          // the partial last block: its rows alone
+          go[u] = !(in_place && from == j + u) && !(tail && j + u == live - 1 && row >= tail);
+          if (go[u]) x[u] = *reinterpret_cast<const uint4 *>(in + from * block_bytes);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kMoveWave; ++u)
+        if (go[u]) {
+          if (is_w && tail && j + u == live - 1) {  // four rows' weights, the live ones of them
+            float *o = reinterpret_cast<float *>(out + (j + u) * block_bytes);
+            const uint32_t y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (row + i < tail) o[i] = __uint_as_float(y[i]);
+          } else {
+            *reinterpret_cast<uint4 *>(out + (j + u) * block_bytes) = x[u];
+          }
+        }
+    }
+    return;
+  }
+  const bool v = s == 2 * pieces + wp + 1;
+  const float *in = (v ? m.vs : m.ks) + bh * nb;
+  float *out = (v ? m.ovs : m.oks) + bh * (m.out_cap / m.bl);
+  for (int j = j0; j < j1; j += kMoveWave) {
+    float x[kMoveWave];
+#pragma unroll
+    for (int u = 0; u < kMoveWave; ++u)
+      if (j + u < j1) x[u] = in[src[j + u]];
+#pragma unroll
+    for (int u = 0; u < kMoveWave; ++u)
+      if (j + u < j1) out[j + u] = x[u];
+  }
+}
+
+// grid (B * H_kv): weights of the rows new_len .. min(len, capacity of out) become 0.
+__global__ void cache8_clear_weights_kernel(float *__restrict__ w, int H_kv, int cap,
+                                            const int32_t *__restrict__ lens) {
+  griddep_wait();
+  griddep_launch();
+  const int b = blockIdx.x / H_kv;
+  const int end = min(lens[2 * b], cap);
+  float *row = w + static_cast<int64_t>(blockIdx.x) * cap;
+  for (int x = lens[2 * b + 1] + threadIdx.x; x < end; x += blockDim.x) row[x] = 0.0f;
+}
+
+}  // namespace msa

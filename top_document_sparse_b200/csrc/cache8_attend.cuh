@@ -1,0 +1,882 @@
+// cache8_attend.cuh -- attention of a query's new tokens over [retrieved memory
+// rows | 8-bit local rows], and the attention weight each cached row received.
+//
+//   s_j = <Q, k_j> / sqrt(D),  p = softmax over the visible rows,  O = sum p_j v_j
+//   weights_j = decay * weights_j + sum over tokens and heads of the group of p_j
+//
+// A few tokens: the bytes of the cache bound it.  Per (query, kv head, context
+// split) CTA, four warps each stream 16-row tiles straight from global memory
+// into the registers of mma.sync m16n8k16: no shared memory and no barrier
+// between tiles.  Context rows are the M rows of S^T = K Q^T and the K rows of
+// O^T += V^T P^T, the (token, head) columns the N columns, so no MMA row is
+// spent on a group's few heads.  The contraction index of an MMA may be
+// permuted freely: lane (g, t) = (lane / 4, lane % 4) reads 16-byte pieces t
+// and t + 4 of rows g and g + 8 of K, and the 16 bytes 16 g .. of rows 2t,
+// 2t+1, 2t+8, 2t+9 of V, and those bytes, widened in place, are its operand
+// fragments (Q is laid out by the same permutation; V's bytes of two rows are
+// interleaved by byte permutes).
+//   Widening: int8 and e4m3 values are exact in fp16, so both MMAs are fp16
+// with the block's scale applied outside: K's to the score; V's to P, as its
+// ratio to the largest V scale seen so far (r), O being kept in units of r.
+// int8 -> fp16 is a byte permute that sets the bits of 1024 + (q + 128) and
+// one subtraction.  Q is scaled by a power of two per column to 1 <= max|q| < 2, which loses
+// nothing of a bf16 row down to 2^-17 of its largest element.  P is kept at
+// 2^11 times its size against a reference maximum that moves only when a score
+// exceeds it by 4 (log2 units): at most 2^15, and rows down to 2^-25 of the
+// largest keep fp16's full 11 bits.
+//   Memory rows are bf16 and go through bf16 MMAs; P is split there into a bf16
+// head and tail, two MMAs, so it loses nothing either.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "cache8.cuh"
+#include "context.cuh"
+
+namespace msa {
+
+constexpr int kC8Warps = 4;
+constexpr float kC8Shift = 11.0f;     // P is 2^11 exp2(s - m)
+constexpr float kC8Slack = 4.0f;      // a score may exceed m by this before m moves
+constexpr float kC8MinUnit = 0x1p-60f;  // smallest unit of O
+
+struct Attend8Args {
+  const void *content;
+  const int32_t *ids;
+  const int64_t *doc_chunk_off;
+  int k, n_docs, table_cap;
+  const uint8_t *k8, *v8;
+  const float *ks, *vs;
+  const int32_t *cache_len, *n_tokens;
+  int H_kv, G, T, cap, bl;
+  const void *Q;
+  float scale_log2;  // log2(e) / sqrt(D)
+  int n_split;
+  void *O;
+  float *lse;
+  float *part_o, *part_ml;
+  float *weights;
+  float decay;
+};
+
+// Query b's tokens and rows; out-of-range lengths count as no tokens.
+struct Attend8Query {
+  int len, n;  // rows in the cache, new tokens (the cache's last n rows)
+};
+__device__ __forceinline__ Attend8Query attend8_query(const Attend8Args &a, int b, bool report) {
+  Attend8Query q;
+  q.len = a.cache_len[b];
+  q.n = a.n_tokens ? a.n_tokens[b] : a.T;
+  if (q.n < 0 || q.n > a.T || q.len < 0 || q.len > a.cap) {
+    if (report) raise_device_error(MSA_DEVERR_BAD_LENGTH);
+    q.len = q.n = 0;
+  }
+  return q;
+}
+
+// D(16x8, f32) += A(16x16, fp16, row) * B(16x8, fp16, col)
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Bytes (0, 1) and (2, 3) of a word as two fp16 pairs.
+template <int FMT>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if constexpr (FMT == MSA_CACHE_INT8) {
+    const uint32_t u = w ^ 0x80808080u;  // q + 128
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
+    uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&x), bias);
+    const __half2 b = __hsub2(*reinterpret_cast<__half2 *>(&y), bias);
+    lo = *reinterpret_cast<const uint32_t *>(&a);
+    hi = *reinterpret_cast<const uint32_t *>(&b);
+  } else {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+        " cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+__device__ __forceinline__ uint4 ld_stream16(const uint8_t *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_stream8(const uint8_t *p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// A 16-row K tile of one head as this lane's bytes: words [row g or g + 8][D / 16].
+template <int D>
+struct KTile {
+  uint32_t w[2][D / 16];
+  // rows >= lim read as zero
+  __device__ __forceinline__ void load(const uint8_t *tile, int lane, int lim) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int p = 0; p < D / 64; ++p) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (g + 8 * r < lim) x = ld_stream16(tile + (g + 8 * r) * D + 64 * p + 16 * t);
+        w[r][4 * p] = x.x; w[r][4 * p + 1] = x.y; w[r][4 * p + 2] = x.z; w[r][4 * p + 3] = x.w;
+      }
+  }
+};
+// A 16-row V tile: words [row 2t, 2t + 1, 2t + 8, 2t + 9][D / 32] of bytes (D / 8) g ...
+template <int D>
+struct VTile {
+  uint32_t w[4][D / 32];
+  __device__ __forceinline__ void load(const uint8_t *tile, int lane, int lim) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+      if constexpr (D == 128) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < lim) x = ld_stream16(tile + row * D + 16 * g);
+        w[r][0] = x.x; w[r][1] = x.y; w[r][2] = x.z; w[r][3] = x.w;
+      } else {
+        uint2 x = make_uint2(0, 0);
+        if (row < lim) x = ld_stream8(tile + row * D + 8 * g);
+        w[r][0] = x.x; w[r][1] = x.y;
+      }
+    }
+  }
+};
+
+// Element of a head that lane-column t holds at k step s, byte 0 (4 consecutive ones follow).
+__device__ __forceinline__ int k_elem(int s, int t) { return (s >> 2) * 64 + 16 * t + 4 * (s & 3); }
+
+// Shared memory of the attention kernel.
+template <int D, int NT>
+struct Attend8Smem {
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kQPitch = D + 8;  // elements of a column's row (16 bytes of padding)
+  static constexpr int kQ = 0;                                   // fp16, scaled
+  static constexpr int kQb = kQ + kCols * kQPitch * 2;           // bf16, as given
+  static constexpr int kColScale = kQb + kCols * kQPitch * 2;    // fp32 per column
+  static constexpr int kMerge = kColScale + kCols * 4;
+  static constexpr int kMergeBytes = kC8Warps * kCols * (D + 4) * 4;  // O, m, l, unit
+  static constexpr int kTable = kMerge + kMergeBytes;            // prefix, bases, chunk table
+  static int bytes(int table_cap) { return kTable + (2 * kMaxTopK + 1 + table_cap) * 4; }
+};
+
+// The columns [c0, c0 + 8 NT) of Q, one warp a column: bf16 as given, fp16 scaled by a power of
+// two to 1 <= max < 2, and that scale times scale_log2.  Columns past the query's tokens are zero.
+template <int D, int NT>
+__device__ __forceinline__ void load_q_columns(const Attend8Args &a, int b, int g, int c0, int n,
+                                               uint8_t *sm) {
+  using Sm = Attend8Smem<D, NT>;
+  __half *qh = reinterpret_cast<__half *>(sm + Sm::kQ);
+  __nv_bfloat16 *qb = reinterpret_cast<__nv_bfloat16 *>(sm + Sm::kQb);
+  float *cs = reinterpret_cast<float *>(sm + Sm::kColScale);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int E = D / 32;
+  for (int c = warp; c < Sm::kCols; c += kC8Warps) {
+    const int cc = c0 + c, t = cc / a.G;
+    __nv_bfloat16 x[E];
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = __float2bfloat16_rn(0.0f);
+    if (t < n) {
+      const __nv_bfloat16 *row =
+          static_cast<const __nv_bfloat16 *>(a.Q) +
+          ((static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc % a.G) * D + lane * E;
+      if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(row);
+      else
+        *reinterpret_cast<uint32_t *>(x) = *reinterpret_cast<const uint32_t *>(row);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) amax = fmaxf(amax, finite_abs(__bfloat162float(x[e])));
+    amax = warp_max(amax);
+    int ex = 0;
+    if (amax > 0.0f) ex = max(-126, min(126, ilogbf(amax)));
+    const float inv = ldexpf(1.0f, -ex);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      qb[c * Sm::kQPitch + lane * E + e] = x[e];
+      qh[c * Sm::kQPitch + lane * E + e] = __float2half_rn(__bfloat162float(x[e]) * inv);
+    }
+    if (lane == 0) cs[c] = ldexpf(a.scale_log2, ex);
+  }
+}
+
+// The running softmax of 8 NT columns over tiles of 16 context rows: lane (g, t) holds rows
+// g, g + 8 and columns 8 nt + 2t, + 1 of S^T.
+template <int D, int NT>
+struct Softmax8 {
+  float m[NT][2], l[NT][2];
+  float acc[NT][D / 16][4];  // O^T, [d pair][col pair], in units of `unit`
+  float unit;
+
+  __device__ __forceinline__ void init() {
+    unit = kC8MinUnit;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.0f;
+    }
+  }
+  // O's unit becomes at least v
+  __device__ __forceinline__ void raise_unit(float v) {
+    if (v > unit) {  // the same in every lane
+      const float f = unit / v;
+      unit = v;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][i][e] *= f;
+    }
+  }
+  // s (log2 units, -inf where hidden) -> p = 2^(s - m + shift), the sums and, where a score
+  // passes its column's reference by more than the slack, new references
+  __device__ __forceinline__ void step(float (&s)[NT][4]) {
+    bool over = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) over = over || s[nt][e] > m[nt][e & 1] + kC8Slack;
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v = fmaxf(s[nt][h], s[nt][2 + h]);
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          const float mn = fmaxf(m[nt][h], v);
+          const float f = mn == -INFINITY ? 1.0f : ex2_approx(m[nt][h] - mn);
+          m[nt][h] = mn;
+          l[nt][h] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            acc[nt][i][h] *= f;
+            acc[nt][i][2 + h] *= f;
+          }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // a column that has seen nothing: -inf - 0, weight 0
+        const float base = (m[nt][h] == -INFINITY ? 0.0f : m[nt][h]) - kC8Shift;
+        s[nt][h] = ex2_approx(s[nt][h] - base);
+        s[nt][2 + h] = ex2_approx(s[nt][2 + h] - base);
+        l[nt][h] += s[nt][h] + s[nt][2 + h];
+      }
+  }
+};
+
+// Rows a column sees: row of its token plus one.
+__device__ __forceinline__ int column_rows(const Attend8Args &a, const Attend8Query &q, int col) {
+  const int t = col / a.G;
+  return t < q.n ? q.len - q.n + t + 1 : 0;
+}
+
+// The CTA's warps (rows of `merge`: [warp][col][D outputs, m, l]) into O and lse, or into the
+// split's partial result.
+template <typename T, int D, int COLS>
+__device__ __forceinline__ void merge_warps(const Attend8Args &a, const Attend8Query &q, int b,
+                                            int g, int c0, int split, const float *merge) {
+  for (int i = threadIdx.x; i < COLS * D; i += 32 * kC8Warps) {
+    const int c = i / D, d = i % D, cc = c0 + c, t = cc / a.G;
+    if (t >= q.n) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kC8Warps; ++w) M = fmaxf(M, merge[(w * COLS + c) * (D + 4) + D]);
+    const float base = M == -INFINITY ? 0.0f : M;
+    float L = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kC8Warps; ++w) {
+      const float *row = merge + (w * COLS + c) * (D + 4);
+      const float f = exp2f(row[D] - base);
+      L += row[D + 1] * f;
+      o += row[d] * f;
+    }
+    const int64_t row = (static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc % a.G;
+    if (a.n_split == 1) {
+      static_cast<T *>(a.O)[row * D + d] = Elem<T>::from_f(L == 0.0f ? 0.0f : o / L);
+      if (d == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
+    } else {
+      a.part_o[(row * a.n_split + split) * D + d] = o;
+      if (d == 0) {
+        a.part_ml[(row * a.n_split + split) * 2] = M;
+        a.part_ml[(row * a.n_split + split) * 2 + 1] = L;
+      }
+    }
+  }
+}
+
+// grid (B * H_kv, n_split, column tiles), block 32 * kC8Warps.
+template <int D, int NT, int FMT>
+__global__ void __launch_bounds__(32 * kC8Warps)
+cache8_attend_kernel(Attend8Args a) {
+  using Sm = Attend8Smem<D, NT>;
+  constexpr int KS = D / 16;  // k steps of S^T
+  constexpr bool kQRegs = NT <= 2;  // Q's fragments stay in registers
+  extern __shared__ __align__(16) uint8_t sm[];
+  const int b = blockIdx.x / a.H_kv, g = blockIdx.x % a.H_kv, split = blockIdx.y;
+  const int c0 = blockIdx.z * Sm::kCols;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, lg = lane >> 2, lt = lane & 3;
+  griddep_wait();
+  griddep_launch();
+  const Attend8Query q = attend8_query(a, b, blockIdx.x % a.H_kv == 0 && split == 0 && c0 == 0 &&
+                                                 threadIdx.x == 0);
+  if (c0 / a.G >= q.n) return;  // padding tokens only (the whole CTA)
+  const int last_col = min(c0 + Sm::kCols, q.n * a.G) - 1;
+  const int n_loc = max(0, column_rows(a, q, last_col));  // rows any column sees
+  const int all_see = column_rows(a, q, c0);              // rows every real column sees
+  const int nl = (n_loc + 15) / 16;
+  const int l0 = static_cast<int>(static_cast<int64_t>(nl) * split / a.n_split);
+  const int l1 = static_cast<int>(static_cast<int64_t>(nl) * (split + 1) / a.n_split);
+  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
+  const uint8_t *kbase = a.k8 + bh * a.cap * D, *vbase = a.v8 + bh * a.cap * D;
+  const float *ks = a.ks + bh * (a.cap / a.bl), *vs = a.vs + bh * (a.cap / a.bl);
+
+  // the first tile is in flight while Q and the chunk table are set up
+  KTile<D> kt;
+  VTile<D> vt;
+  float ksc = 0.0f, vsc = 0.0f;
+  int tile = l0 + warp;
+  if (tile < l1) {
+    kt.load(kbase + static_cast<int64_t>(tile) * 16 * D, lane, n_loc - tile * 16);
+    vt.load(vbase + static_cast<int64_t>(tile) * 16 * D, lane, n_loc - tile * 16);
+    ksc = ks[tile * 16 / a.bl];
+    vsc = vs[tile * 16 / a.bl];
+  }
+  load_q_columns<D, NT>(a, b, g, c0, q.n, sm);
+  int *pre = reinterpret_cast<int *>(sm + Sm::kTable), *base = pre + kMaxTopK + 1;
+  int *table = base + kMaxTopK;
+  int n_mem = 0;
+  if (a.k > 0)
+    n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
+                              nullptr, 0, table, pre, base, a.table_cap);
+  __syncthreads();
+
+  const __half *qh = reinterpret_cast<const __half *>(sm + Sm::kQ);
+  const float *cs = reinterpret_cast<const float *>(sm + Sm::kColScale);
+  uint32_t qf[kQRegs ? NT : 1][KS][2];
+  if constexpr (kQRegs) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(qh + (8 * nt + lg) * Sm::kQPitch + k_elem(s, lt));
+        qf[nt][s][0] = x.x;
+        qf[nt][s][1] = x.y;
+      }
+  }
+  float colf[NT][2];  // score factor of this lane's columns
+  int rows[NT][2];    // rows they see
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      colf[nt][h] = cs[8 * nt + 2 * lt + h];
+      rows[nt][h] = column_rows(a, q, c0 + 8 * nt + 2 * lt + h);
+    }
+  Softmax8<D, NT> st;
+  st.init();
+
+  // ---- local rows
+  for (; tile < l1; tile += kC8Warps) {
+    const int next = tile + kC8Warps;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      uint32_t a0, a1, a2, a3;
+      widen4<FMT>(kt.w[0][i], a0, a2);
+      widen4<FMT>(kt.w[1][i], a1, a3);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (kQRegs) {
+          mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][i][0], qf[nt][i][1]);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2 *>(qh + (8 * nt + lg) * Sm::kQPitch + k_elem(i, lt));
+          mma_f16_16816(s[nt], a0, a1, a2, a3, x.x, x.y);
+        }
+      }
+    }
+    const float k_scale = ksc, v_scale = vsc;
+    if (next < l1) {  // K's registers are free: the next tile's
+      kt.load(kbase + static_cast<int64_t>(next) * 16 * D, lane, n_loc - next * 16);
+      ksc = ks[next * 16 / a.bl];
+      vsc = vs[next * 16 / a.bl];
+    }
+    const int x0 = tile * 16;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] *= colf[nt][e & 1] * k_scale;
+    if (x0 + 16 > all_see) {  // rows that some column does not see
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (x0 + lg + 8 * (e >> 1) >= rows[nt][e & 1]) s[nt][e] = -INFINITY;
+    }
+    st.step(s);
+    st.raise_unit(v_scale);
+    const float ratio = v_scale / st.unit;
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      pb[nt][0] = movmatrix_trans(pack_f16x2(s[nt][0] * ratio, s[nt][1] * ratio));
+      pb[nt][1] = movmatrix_trans(pack_f16x2(s[nt][2] * ratio, s[nt][3] * ratio));
+    }
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      // words w of four rows: elements (D / 8) g + 4 w .. + 3, two M tiles
+      uint32_t lo[2][2], hi[2][2];  // [row pair][element pair of the word]
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t e01 = __byte_perm(vt.w[2 * r][w], vt.w[2 * r + 1][w], 0x5140);
+        const uint32_t e23 = __byte_perm(vt.w[2 * r][w], vt.w[2 * r + 1][w], 0x7362);
+        widen4<FMT>(e01, lo[r][0], hi[r][0]);
+        widen4<FMT>(e23, lo[r][1], hi[r][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16_16816(st.acc[nt][2 * w + i], lo[0][i], hi[0][i], lo[1][i], hi[1][i], pb[nt][0],
+                        pb[nt][1]);
+    }
+    if (next < l1) vt.load(vbase + static_cast<int64_t>(next) * 16 * D, lane, n_loc - next * 16);
+  }
+
+  // ---- memory rows: every column sees them
+  const int nm = (n_mem + 15) / 16;
+  const int m1 = static_cast<int>(static_cast<int64_t>(nm) * (split + 1) / a.n_split);
+  const __nv_bfloat16 *qb = reinterpret_cast<const __nv_bfloat16 *>(sm + Sm::kQb);
+  const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
+  const float to_unit = 1.0f / st.unit;
+  for (int mt = static_cast<int>(static_cast<int64_t>(nm) * split / a.n_split) + warp; mt < m1;
+       mt += kC8Warps) {
+    const int x0 = mt * 16;
+    auto row_ptr = [&](int x) {
+      return static_cast<const __nv_bfloat16 *>(a.content) +
+             static_cast<int64_t>(table[min(x, n_mem - 1)]) * 2 * kv + g * D;
+    };
+    const __nv_bfloat16 *k0 = row_ptr(x0 + lg), *k1 = row_ptr(x0 + lg + 8);
+    const __nv_bfloat16 *v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = row_ptr(x0 + 2 * lt + (r & 1) + 8 * (r >> 1)) + kv + (D / 8) * lg;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KS; i += 2) {  // two k steps: 8 elements of a row
+      const uint4 x0v = *reinterpret_cast<const uint4 *>(k0 + k_elem(i, lt));
+      const uint4 x1v = *reinterpret_cast<const uint4 *>(k1 + k_elem(i, lt));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const __nv_bfloat16 *qr = qb + (8 * nt + lg) * Sm::kQPitch;
+        const uint2 b0 = *reinterpret_cast<const uint2 *>(qr + k_elem(i, lt));
+        const uint2 b1 = *reinterpret_cast<const uint2 *>(qr + k_elem(i + 1, lt));
+        mma_bf16_16816(s[nt], x0v.x, x1v.x, x0v.y, x1v.y, b0.x, b0.y);
+        mma_bf16_16816(s[nt], x0v.z, x1v.z, x0v.w, x1v.w, b1.x, b1.y);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = (c0 + 8 * nt + 2 * lt + (e & 1)) / a.G;
+        const bool ok = x0 + lg + 8 * (e >> 1) < n_mem && t < q.n;
+        s[nt][e] = ok ? s[nt][e] * a.scale_log2 : -INFINITY;
+      }
+    st.step(s);
+    uint32_t pb[NT][2][2];  // [part][row half]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float p0 = s[nt][2 * r] * to_unit, p1 = s[nt][2 * r + 1] * to_unit;
+        const uint32_t head = pack_bf16x2(p0, p1);
+        pb[nt][0][r] = movmatrix_trans(head);
+        pb[nt][1][r] = movmatrix_trans(pack_bf16x2(p0 - __uint_as_float(head << 16),
+                                                   p1 - __uint_as_float(head & 0xffff0000u)));
+      }
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {  // 8 elements of four rows: four M tiles
+      uint32_t x[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint4 y = *reinterpret_cast<const uint4 *>(v[r] + 8 * c);
+        x[r][0] = y.x; x[r][1] = y.y; x[r][2] = y.z; x[r][3] = y.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = __byte_perm(x[0][i], x[1][i], 0x5410), a1 = __byte_perm(x[0][i], x[1][i], 0x7632);
+        const uint32_t a2 = __byte_perm(x[2][i], x[3][i], 0x5410), a3 = __byte_perm(x[2][i], x[3][i], 0x7632);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_bf16_16816(st.acc[nt][4 * c + i], a0, a1, a2, a3, pb[nt][0][0], pb[nt][0][1]);
+          mma_bf16_16816(st.acc[nt][4 * c + i], a0, a1, a2, a3, pb[nt][1][0], pb[nt][1][1]);
+        }
+      }
+    }
+  }
+
+  // ---- the warps meet
+  float *merge = reinterpret_cast<float *>(sm + Sm::kMerge);
+  const float out = st.unit * exp2f(-kC8Shift);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float L = st.l[nt][h];
+      L += __shfl_xor_sync(0xffffffffu, L, 4);
+      L += __shfl_xor_sync(0xffffffffu, L, 8);
+      L += __shfl_xor_sync(0xffffffffu, L, 16);
+      float *row = merge + (warp * Sm::kCols + 8 * nt + 2 * lt + h) * (D + 4);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        row[(D / 8) * lg + 2 * i] = st.acc[nt][i][h] * out;
+        row[(D / 8) * lg + 2 * i + 1] = st.acc[nt][i][2 + h] * out;
+      }
+      if (lg == 0) {
+        row[D] = st.m[nt][h];
+        row[D + 1] = L * exp2f(-kC8Shift);
+      }
+    }
+  __syncthreads();
+  merge_warps<__nv_bfloat16, D, Sm::kCols>(a, q, b, g, c0, split, merge);
+}
+
+// ---------------------------------------------------------------- fp32
+// Memories of fp32: CUDA cores, four columns a CTA.  Scores with a lane on each of 32 context
+// rows, outputs with a lane on D / 32 elements; sums in fp32.
+constexpr int kC8Cols32 = 4;
+template <int D>
+struct Attend8Smem32 {
+  static constexpr int kQ = 0;
+  static constexpr int kMerge = kQ + kC8Cols32 * D * 4;
+  static constexpr int kTable = kMerge + kC8Warps * kC8Cols32 * (D + 4) * 4;
+  static int bytes(int table_cap) { return kTable + (2 * kMaxTopK + 1 + table_cap) * 4; }
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(32 * kC8Warps)
+cache8_attend_f32_kernel(Attend8Args a) {
+  using Sm = Attend8Smem32<D>;
+  constexpr int C = kC8Cols32, E = D / 32;
+  extern __shared__ __align__(16) uint8_t sm[];
+  const int b = blockIdx.x / a.H_kv, g = blockIdx.x % a.H_kv, split = blockIdx.y;
+  const int c0 = blockIdx.z * C;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  griddep_wait();
+  griddep_launch();
+  const Attend8Query q = attend8_query(a, b, blockIdx.x % a.H_kv == 0 && split == 0 && c0 == 0 &&
+                                                 threadIdx.x == 0);
+  if (c0 / a.G >= q.n) return;
+  float *qs = reinterpret_cast<float *>(sm + Sm::kQ);
+  for (int i = threadIdx.x; i < C * D; i += 32 * kC8Warps) {
+    const int cc = c0 + i / D, t = cc / a.G;
+    qs[i] = t < q.n ? static_cast<const float *>(a.Q)[((static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G +
+                                                       g * a.G + cc % a.G) * D + i % D] * a.scale_log2
+                    : 0.0f;
+  }
+  int *pre = reinterpret_cast<int *>(sm + Sm::kTable), *base = pre + kMaxTopK + 1;
+  int *table = base + kMaxTopK;
+  int n_mem = 0;
+  if (a.k > 0)
+    n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
+                              nullptr, 0, table, pre, base, a.table_cap);
+  __syncthreads();
+  const int last_col = min(c0 + C, q.n * a.G) - 1;
+  const int n_loc = max(0, column_rows(a, q, last_col));
+  const int nl = (n_loc + 31) / 32, nm = (n_mem + 31) / 32, n = nl + nm;
+  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
+  const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
+  int rows[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) rows[c] = c0 + c <= last_col ? column_rows(a, q, c0 + c) : 0;
+  float m[C], l[C], acc[C][E];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    m[c] = -INFINITY;
+    l[c] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[c][e] = 0.0f;
+  }
+  const int i1 = static_cast<int>(static_cast<int64_t>(n) * (split + 1) / a.n_split);
+  for (int i = static_cast<int>(static_cast<int64_t>(n) * split / a.n_split) + warp; i < i1;
+       i += kC8Warps) {
+    const bool loc = i < nl;
+    const int x0 = (loc ? i : i - nl) * 32, x = x0 + lane;
+    const int lim = loc ? n_loc : n_mem;
+    float s[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] = 0.0f;
+    if (x < lim) {
+      if (loc) {
+        const uint8_t *kr = a.k8 + (bh * a.cap + x) * D;
+        const float sc = a.ks[bh * (a.cap / a.bl) + x / a.bl];
+#pragma unroll 2
+        for (int p = 0; p < D / 16; ++p) {
+          float kx[16];
+          unpack16<FMT>(*reinterpret_cast<const uint4 *>(kr + 16 * p), sc, kx);
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[c] = fmaf(qs[c * D + 16 * p + e], kx[e], s[c]);
+        }
+      } else {
+        const float *kr = static_cast<const float *>(a.content) + static_cast<int64_t>(table[x]) * 2 * kv + g * D;
+#pragma unroll 2
+        for (int p = 0; p < D / 4; ++p) {
+          float kx[4];
+          load4(kr + 4 * p, kx);
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[c] = fmaf(qs[c * D + 4 * p + e], kx[e], s[c]);
+        }
+      }
+    }
+    float f[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const bool see = loc ? x < rows[c] : (x < lim && c0 + c <= last_col);
+      if (!see) s[c] = -INFINITY;
+      const float mn = fmaxf(m[c], warp_max(s[c]));
+      const float ref = mn == -INFINITY ? 0.0f : mn;
+      f[c] = mn == -INFINITY ? 1.0f : exp2f(m[c] - mn);
+      m[c] = mn;
+      s[c] = exp2f(s[c] - ref);
+      l[c] = l[c] * f[c] + s[c];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[c][e] *= f[c];
+    }
+    const int cnt = min(32, lim - x0);
+    for (int r = 0; r < cnt; ++r) {
+      float vx[4];
+      if (loc) {
+        const int64_t row = bh * a.cap + x0 + r;
+        const float sc = a.vs[bh * (a.cap / a.bl) + (x0 + r) / a.bl];
+        uint32_t w;
+        if constexpr (E == 4)
+          w = *reinterpret_cast<const uint32_t *>(a.v8 + row * D + 4 * lane);
+        else
+          w = *reinterpret_cast<const uint16_t *>(a.v8 + row * D + 2 * lane);
+        Fmt8<FMT>::unpack4(w, vx);
+#pragma unroll
+        for (int e = 0; e < E; ++e) vx[e] *= sc;
+      } else {
+        const float *vr = static_cast<const float *>(a.content) +
+                          static_cast<int64_t>(table[x0 + r]) * 2 * kv + kv + g * D + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) vx[e] = vr[e];
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float p = __shfl_sync(0xffffffffu, s[c], r);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[c][e] = fmaf(p, vx[e], acc[c][e]);
+      }
+    }
+  }
+  float *merge = reinterpret_cast<float *>(sm + Sm::kMerge);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float *row = merge + (warp * C + c) * (D + 4);
+    const float L = warp_sum(l[c]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) row[E * lane + e] = acc[c][e];
+    if (lane == 0) {
+      row[D] = m[c];
+      row[D + 1] = L;
+    }
+  }
+  __syncthreads();
+  merge_warps<float, D, C>(a, q, b, g, c0, split, merge);
+}
+
+// ---------------------------------------------------------------- combine
+// grid (B * T * H_q), block D: merge the context splits.
+template <typename T>
+__global__ void cache8_combine_kernel(Attend8Args a, int D) {
+  griddep_wait();
+  griddep_launch();
+  const int64_t row = blockIdx.x;
+  const int H_q = a.H_kv * a.G;
+  const int b = static_cast<int>(row / H_q / a.T), t = static_cast<int>(row / H_q % a.T);
+  const Attend8Query q = attend8_query(a, b, false);
+  if (t >= q.n) return;
+  const float *ml = a.part_ml + row * a.n_split * 2;
+  float M = -INFINITY;
+  for (int s = 0; s < a.n_split; ++s) M = fmaxf(M, ml[2 * s]);
+  const float base = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f, o = 0.0f;
+  for (int s = 0; s < a.n_split; ++s) {
+    const float f = exp2f(ml[2 * s] - base);
+    L += ml[2 * s + 1] * f;
+    o += a.part_o[(row * a.n_split + s) * D + threadIdx.x] * f;
+  }
+  static_cast<T *>(a.O)[row * D + threadIdx.x] = Elem<T>::from_f(L == 0.0f ? 0.0f : o / L);
+  if (threadIdx.x == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
+}
+
+// ---------------------------------------------------------------- weights
+// The weight each cached row received: with the softmax's log-sum known, a second pass over K
+// alone recomputes the scores, p = 2^(s - lse), and sums them over the columns.  A warp keeps
+// 16 rows as MMA operands and walks over all columns, staged 8 NT at a time in shared memory.
+// grid (ceil(cap / 64), B * H_kv), block 32 * kC8Warps.  fp32 memories: see below.
+template <int D, int NT, int FMT>
+__global__ void __launch_bounds__(32 * kC8Warps)
+cache8_weight_kernel(Attend8Args a) {
+  using Sm = Attend8Smem<D, NT>;
+  constexpr int KS = D / 16;
+  __shared__ __align__(16) uint8_t sm[Sm::kMerge];
+  __shared__ float lse2[Sm::kCols];
+  griddep_wait();
+  griddep_launch();
+  const int b = blockIdx.y / a.H_kv, g = blockIdx.y % a.H_kv;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, lg = lane >> 2, lt = lane & 3;
+  const Attend8Query q = attend8_query(a, b, false);
+  if (static_cast<int>(blockIdx.x) * 64 >= q.len) return;
+  const int x0 = blockIdx.x * 64 + warp * 16;
+  const bool work = x0 < q.len;
+  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
+  uint32_t ka[KS][4];
+  float k_scale = 0.0f;
+  if (work) {
+    KTile<D> kt;
+    kt.load(a.k8 + (bh * a.cap + x0) * D, lane, q.len - x0);
+    k_scale = a.ks[bh * (a.cap / a.bl) + x0 / a.bl];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      widen4<FMT>(kt.w[0][i], ka[i][0], ka[i][2]);
+      widen4<FMT>(kt.w[1][i], ka[i][1], ka[i][3]);
+    }
+  }
+  const __half *qh = reinterpret_cast<const __half *>(sm + Sm::kQ);
+  const float *cs = reinterpret_cast<const float *>(sm + Sm::kColScale);
+  float sum[2] = {0.0f, 0.0f};
+  for (int c0 = 0; c0 < q.n * a.G; c0 += Sm::kCols) {
+    if (c0) __syncthreads();
+    load_q_columns<D, NT>(a, b, g, c0, q.n, sm);
+    for (int c = threadIdx.x; c < Sm::kCols; c += 32 * kC8Warps) {
+      const int cc = c0 + c, t = cc / a.G;
+      float v = INFINITY;  // no token, or one that sees nothing: weight 0
+      if (t < q.n) {
+        const float x = a.lse[(static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc % a.G];
+        if (x != -INFINITY) v = x * kLog2e;
+      }
+      lse2[c] = v;
+    }
+    __syncthreads();
+    if (!work) continue;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(qh + (8 * nt + lg) * Sm::kQPitch + k_elem(i, lt));
+        mma_f16_16816(s, ka[i][0], ka[i][1], ka[i][2], ka[i][3], x.x, x.y);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = 8 * nt + 2 * lt + (e & 1), row = x0 + lg + 8 * (e >> 1);
+        const float p = exp2f(s[e] * (cs[c] * k_scale) - lse2[c]);
+        sum[e >> 1] += row < column_rows(a, q, c0 + c) ? p : 0.0f;
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+    const int row = x0 + lg + 8 * r;
+    if (work && lt == 0 && row < q.len) {
+      float *w = a.weights + bh * a.cap + row;
+      *w = a.decay == 0.0f ? sum[r] : a.decay * *w + sum[r];
+    }
+  }
+}
+
+// The same on CUDA cores: a lane on each of 32 rows, Q broadcast from shared memory.
+template <int D, int FMT>
+__global__ void __launch_bounds__(32 * kC8Warps)
+cache8_weight_f32_kernel(Attend8Args a) {
+  __shared__ __align__(16) float qs[kC8Cols32 * D];
+  __shared__ float lse2[kC8Cols32];
+  griddep_wait();
+  griddep_launch();
+  const int b = blockIdx.y / a.H_kv, g = blockIdx.y % a.H_kv;
+  const Attend8Query q = attend8_query(a, b, false);
+  const int x = blockIdx.x * 32 * kC8Warps + threadIdx.x;
+  if (static_cast<int>(blockIdx.x) * 32 * kC8Warps >= q.len) return;
+  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
+  const bool work = x < q.len;
+  const uint8_t *kr = a.k8 + (bh * a.cap + (work ? x : 0)) * D;
+  const float sc = work ? a.ks[bh * (a.cap / a.bl) + x / a.bl] : 0.0f;
+  float sum = 0.0f;
+  for (int c0 = 0; c0 < q.n * a.G; c0 += kC8Cols32) {
+    if (c0) __syncthreads();
+    for (int i = threadIdx.x; i < kC8Cols32 * D; i += 32 * kC8Warps) {
+      const int cc = c0 + i / D, t = cc / a.G;
+      const int64_t row = (static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc % a.G;
+      qs[i] = t < q.n ? static_cast<const float *>(a.Q)[row * D + i % D] * a.scale_log2 : 0.0f;
+      if (i % D == 0) {
+        float v = INFINITY;
+        if (t < q.n && a.lse[row] != -INFINITY) v = a.lse[row] * kLog2e;
+        lse2[i / D] = v;
+      }
+    }
+    __syncthreads();
+    if (!work) continue;
+    float s[kC8Cols32] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+    for (int p = 0; p < D / 16; ++p) {
+      float kx[16];
+      unpack16<FMT>(*reinterpret_cast<const uint4 *>(kr + 16 * p), sc, kx);
+#pragma unroll
+      for (int c = 0; c < kC8Cols32; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[c] = fmaf(qs[c * D + 16 * p + e], kx[e], s[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kC8Cols32; ++c)
+      sum += x < column_rows(a, q, c0 + c) ? exp2f(s[c] - lse2[c]) : 0.0f;
+  }
+  if (work) {
+    float *w = a.weights + bh * a.cap + x;
+    *w = a.decay == 0.0f ? sum : a.decay * *w + sum;
+  }
+}
+
+}  // namespace msa

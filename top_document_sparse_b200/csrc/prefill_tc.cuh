@@ -95,61 +95,6 @@ __device__ __forceinline__ uint32_t ptc_swz(int r, int c, int rows) {
   return static_cast<uint32_t>((c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// The chunk table of query b built by one warp (the loader): table[x] = chunk
-// row of context row x < n_mem, ranks in order; the same rows as
-// build_chunk_table.  Returns n_mem in every lane.
-__device__ __forceinline__ int build_chunk_table_warp(const int32_t *__restrict__ ids_b, int k,
-                                                      const int64_t *__restrict__ doc_chunk_off,
-                                                      int n_docs, const int32_t *__restrict__ slots_b,
-                                                      int slot_chunks, int *table, int *pre,
-                                                      int *base, int table_cap, int lane) {
-  int cnt[2] = {0, 0};
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = lane + 32 * h;
-    if (r < k) {
-      const int d = ids_b[r];
-      if (d >= 0 && d < n_docs) {
-        const int64_t c0 = doc_chunk_off[d];
-        cnt[h] = static_cast<int>(doc_chunk_off[d + 1] - c0);
-        base[r] = slots_b ? slots_b[r] * slot_chunks : static_cast<int>(c0);
-      } else {
-        raise_device_error(MSA_DEVERR_BAD_DOC_ID);
-        base[r] = 0;
-      }
-    }
-  }
-  int run = 0;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    int v = cnt[h];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    const int r = lane + 32 * h;
-    const int excl = run + v - cnt[h];
-    // (a rank that would overflow the table contributes nothing; host validation keeps
-    // k * max_doc_chunks <= table_cap)
-    if (r < k) pre[r] = excl + cnt[h] > table_cap ? min(excl, table_cap) : excl;
-    run += __shfl_sync(0xffffffffu, v, 31);
-  }
-  const int n_mem = min(run, table_cap);
-  if (lane == 0) pre[k] = n_mem;
-  __syncwarp();
-  for (int x = lane; x < n_mem; x += 32) {
-    int lo = 0, hi = k - 1;  // last rank r with pre[r] <= x
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= x) lo = mid; else hi = mid - 1;
-    }
-    table[x] = base[lo] + (x - pre[lo]);
-  }
-  __syncwarp();
-  return n_mem;
-}
-
 // grid n_pairs * B * H_kv (n_pairs = ceil(ceil(T * G / 128) / 2)), block
 // kPtcThreads, one CTA per SM: the tile pairs of one (query, kv head) are
 // adjacent in launch order, so they run at about the same time and read the

@@ -18,6 +18,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 
 MSA_F32, MSA_BF16 = 0, 1
 DEVERR_BAD_DOC_ID, DEVERR_CACHE_OVERFLOW, DEVERR_WAIT_TIMEOUT = 0x1, 0x2, 0x4
+DEVERR_BAD_LENGTH = 0x8
 STATUS = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_CUDA",
           4: "MSA_ERR_OUT_OF_MEMORY", 5: "MSA_ERR_TIMEOUT", 6: "MSA_ERR_STATE"}
 _DTYPE = {torch.float32: MSA_F32, torch.bfloat16: MSA_BF16}
@@ -53,6 +54,21 @@ class DecodeState(ctypes.Structure):
                 ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
                 ("cache_len", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t)]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("theta", ctypes.c_double), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_length", ctypes.c_int64), ("magnitude", ctypes.c_double)]
+
+
+class Cache8Struct(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("capacity", ctypes.c_int32),
+                ("block_len", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("cache_len", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -97,6 +113,18 @@ SIGNATURES = {
     "msa_route_backward": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _P, _P, _P, _P]),
     "msa_sparse_attend_backward": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _P,
                                                   _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P]),
+    "msa_rope_create": (ctypes.c_int, [ctypes.POINTER(RopeConfig), ctypes.POINTER(_P)]),
+    "msa_rope_destroy": (ctypes.c_int, [_P]),
+    "msa_rope_apply": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I32, _P, _I32, _I64, _P, _I64,
+                                      _P, _I32, _I64, _P, _I64, _P]),
+    "msa_cache8_append": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P,
+                                         _P]),
+    "msa_cache8_read": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _P]),
+    "msa_cache8_attend_workspace_size": (_SZ, [_P, _P, _I32, _I32, _I32]),
+    "msa_cache8_attend": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P, _P,
+                                         ctypes.c_float, _P, _SZ, _P]),
+    "msa_cache8_evict_workspace_size": (_SZ, [_P, _P]),
+    "msa_cache8_evict": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _P, _SZ, _P]),
     "msa_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _P]),
     "msa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "msa_last_error": (ctypes.c_char_p, []),
@@ -432,3 +460,249 @@ class LayerDecode:
                              k_cache=_ptr(self.k_cache), v_cache=_ptr(self.v_cache),
                              cache_len=_ptr(self.cache_len), workspace=_ptr(self.workspace),
                              workspace_bytes=self.workspace.numel())
+
+
+def _tensor(t, name: str, shape, dtype, device, contiguous: bool = True) -> int:
+    """Check one argument of the rotary and 8-bit cache calls; its device pointer."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _call(fn, device, stream, *args):
+    """One library call on `device` (made current for it) and `stream` (default: its current one)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    if status != 0:
+        _check(status)
+
+
+def _device(device) -> torch.device:
+    d = torch.device(device)
+    if d.type != "cuda":
+        raise ValueError(f"expected a CUDA device, got {d}")
+    return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+class Rope:
+    """Rotary positions of Q and K (msa_rope_*): the first ``rotary_dim`` elements of each head
+    (None: all) in "half" or "interleaved" pairs, frequencies of base ``theta`` with scaling
+    "none", "linear", "ntk" or "yarn".  The output feeds Cache8.append and Cache8.attend.
+
+    q and k are [..., heads, head_dim] with the same leading dimensions as ``positions`` (int64),
+    fp32 or bf16; heads of a token are dense and tokens evenly spaced, so slices of a joint
+    projection are taken as they lie.  k may be None."""
+
+    LAYOUTS = {"half": 0, "interleaved": 1}
+    SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+    def __init__(self, head_dim: int, rotary_dim: int | None = None, theta: float = 1e6,
+                 layout: str = "half", scaling: str = "none", factor: float = 1.0,
+                 original_length: int = 0, magnitude: float = 0.0, device="cuda"):
+        if layout not in self.LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(self.LAYOUTS)}, got {layout!r}")
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(self.SCALINGS)}, got {scaling!r}")
+        cfg = RopeConfig(head_dim=head_dim, rotary_dim=head_dim if rotary_dim is None else rotary_dim,
+                         theta=theta, layout=self.LAYOUTS[layout], scaling=self.SCALINGS[scaling],
+                         factor=factor, original_length=original_length, magnitude=magnitude)
+        h = _P()
+        self.handle = None
+        self.device = _device(device)
+        with torch.cuda.device(self.device):
+            _check(_lib.msa_rope_create(ctypes.byref(cfg), ctypes.byref(h)))
+        self.handle = h
+        self.head_dim = head_dim
+
+    def close(self):
+        if getattr(self, "handle", None):
+            _check(_lib.msa_rope_destroy(self.handle))
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _side(self, x, name, lead, dtype):
+        """(pointer, heads, token stride) of one of Q and K."""
+        _tensor(x, name, lead + x.shape[-2:], dtype, self.device, contiguous=False)
+        H, D = x.shape[-2:]
+        st = x.stride()
+        if D != self.head_dim:
+            raise ValueError(f"{name}: expected head_dim {self.head_dim}, got {D}")
+        ok = st[-1] == 1 and (H == 1 or st[-2] == D)
+        step = H * D  # distance of consecutive tokens
+        if len(lead) and lead.numel() > 1:
+            n, step = 1, None
+            for d in range(len(lead) - 1, -1, -1):
+                if lead[d] == 1:
+                    continue
+                if step is None:
+                    step = st[d]
+                ok = ok and st[d] == n * step
+                n *= lead[d]
+        if not ok:
+            raise ValueError(f"{name}: heads must be dense and tokens evenly spaced")
+        return x.data_ptr(), H, step
+
+    def _apply(self, inverse, q, k, positions, q_out, k_out, stream):
+        lead = positions.shape
+        pos = _tensor(positions, "positions", lead, torch.int64, self.device)
+        if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE:
+            raise TypeError("q: expected an fp32 or bf16 torch.Tensor")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qp, qh, qs = self._side(q, "q", lead, q.dtype)
+        qo, qoh, qos = self._side(q_out, "q_out", lead, q.dtype)
+        kp, kh, ks, ko, koh, kos = None, 0, 0, None, 0, 0
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            kp, kh, ks = self._side(k, "k", lead, q.dtype)
+            ko, koh, kos = self._side(k_out, "k_out", lead, q.dtype)
+        if qoh != qh or koh != kh:
+            raise ValueError("the outputs must have the heads of the inputs")
+        _call(_lib.msa_rope_apply, self.device, stream, self.handle, _DTYPE[q.dtype],
+              positions.numel(), pos, inverse, qp, qh, qs, qo, qos, kp, kh, ks, ko, kos)
+        return q_out, k_out
+
+    def rotate(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        """Rotated (q, k); outputs may be given, and may be the inputs themselves."""
+        return self._apply(0, q, k, positions, q_out, k_out, stream)
+
+    def backward(self, d_q, d_k, positions, dq_out=None, dk_out=None, stream=None):
+        """Gradients of rotate's inputs from the gradients of its outputs."""
+        return self._apply(1, d_q, d_k, positions, dq_out, dk_out, stream)
+
+
+class Cache8:
+    """8-bit local K/V cache of one layer (msa_cache8_*), buffers torch-allocated: ``k``, ``v``
+    [batch][H_kv][capacity][D] (int8 or float8_e4m3fn), ``k_scale``, ``v_scale`` fp32
+    [batch][H_kv][capacity / block_len], ``cache_len`` int32 [batch] and, with ``track_weights``,
+    ``weights`` fp32 [batch][H_kv][capacity]."""
+
+    FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
+
+    def __init__(self, mem: Memory, batch: int, capacity: int, block_len: int = 64,
+                 fmt: str = "int8", track_weights: bool = False, device="cuda"):
+        if fmt not in self.FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(self.FORMATS)}, got {fmt!r}")
+        if block_len not in (16, 32, 64, 128):
+            raise ValueError(f"block_len must be 16, 32, 64 or 128, got {block_len}")
+        if batch < 1 or capacity < 1 or capacity % block_len:
+            raise ValueError(f"capacity={capacity} must be a positive multiple of block_len="
+                             f"{block_len}, and batch={batch} positive")
+        self.mem, self.batch, self.capacity, self.block_len = mem, batch, capacity, block_len
+        self.fmt = fmt
+        self.device = dev = _device(device)
+        code, dtype = self.FORMATS[fmt]
+        H, D = mem.n_kv_heads, mem.head_dim
+        self.k = torch.zeros(batch, H, capacity, D, dtype=torch.int8, device=dev).view(dtype)
+        self.v = torch.zeros(batch, H, capacity, D, dtype=torch.int8, device=dev).view(dtype)
+        self.k_scale = torch.zeros(batch, H, capacity // block_len, device=dev)
+        self.v_scale = torch.zeros_like(self.k_scale)
+        self.cache_len = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self.weights = torch.zeros(batch, H, capacity, device=dev) if track_weights else None
+        self.c = Cache8Struct(batch=batch, capacity=capacity, block_len=block_len, format=code,
+                              k=self.k.data_ptr(), v=self.v.data_ptr(),
+                              k_scale=self.k_scale.data_ptr(), v_scale=self.v_scale.data_ptr(),
+                              cache_len=self.cache_len.data_ptr(),
+                              weights=self.weights.data_ptr() if track_weights else None)
+        self._ref = ctypes.byref(self.c)
+
+    def _counts(self, t, name):
+        return None if t is None else _tensor(t, name, (self.batch,), torch.int32, self.device)
+
+    def append(self, K, V, n_tokens=None, start=None, stream=None):
+        """Append [batch][tokens][H_kv][D] rows, K already rotated (msa_cache8_append).  K and V
+        may be slices of a joint projection (H_kv and D dense, rows on 16 bytes)."""
+        mem = self.mem
+        if K.dim() != 4:
+            raise ValueError("K: expected [batch][tokens][H_kv][D]")
+        T = K.shape[1]
+        shape = (self.batch, T, mem.n_kv_heads, mem.head_dim)
+        kp = _tensor(K, "K", shape, mem.dtype, self.device, contiguous=False)
+        vp = _tensor(V, "V", shape, mem.dtype, self.device, contiguous=False)
+        ks, vs = K.stride(), V.stride()
+        for st in (ks, vs):
+            if st[3] != 1 or (st[2] != mem.head_dim and mem.n_kv_heads > 1):
+                raise ValueError("K, V: the heads of a token must be dense")
+        _call(_lib.msa_cache8_append, self.device, stream, mem.handle, self._ref, kp, vp, T,
+              ks[0] if self.batch > 1 else 0, ks[1] if T > 1 else 0,
+              vs[0] if self.batch > 1 else 0, vs[1] if T > 1 else 0,
+              self._counts(n_tokens, "n_tokens"), self._counts(start, "start"))
+
+    def read(self, begin, rows: int, K_out=None, V_out=None, stream=None):
+        """Values of rows begin[b] .. begin[b] + rows - 1 (begin None: from 0) in the memory's
+        dtype, token-major [batch][rows][H_kv][D] like the framework's caches; zeros past
+        cache_len."""
+        mem = self.mem
+        shape = (self.batch, rows, mem.n_kv_heads, mem.head_dim)
+        if K_out is None:
+            K_out = torch.empty(shape, dtype=mem.dtype, device=self.device)
+        if V_out is None:
+            V_out = torch.empty(shape, dtype=mem.dtype, device=self.device)
+        _call(_lib.msa_cache8_read, self.device, stream, mem.handle, self._ref,
+              self._counts(begin, "begin"), rows,
+              _tensor(K_out, "K_out", shape, mem.dtype, self.device),
+              _tensor(V_out, "V_out", shape, mem.dtype, self.device))
+        return K_out, V_out
+
+    def attend_workspace_size(self, tokens: int, k: int, n_q_heads: int) -> int:
+        return _lib.msa_cache8_attend_workspace_size(self.mem.handle, self._ref, tokens, k,
+                                                     n_q_heads)
+
+    def attend(self, content, ids, Q, O, workspace, lse=None, n_tokens=None, weight_decay=None,
+               stream=None):
+        """Attention of the cache's newest tokens over the retrieved memory rows and the cached
+        rows (msa_cache8_attend): Q, O [batch][tokens][n_q_heads][D], Q already rotated; lse
+        [batch][tokens][n_q_heads] optional.  weight_decay None leaves ``weights`` alone."""
+        mem, dev = self.mem, self.device
+        if Q.dim() != 4:
+            raise ValueError("Q: expected [batch][tokens][n_q_heads][D]")
+        T, H_q = Q.shape[1], Q.shape[2]
+        shape = (self.batch, T, H_q, mem.head_dim)
+        k = ids.shape[1] if ids is not None else 0
+        if weight_decay is not None and not weight_decay >= 0.0:
+            raise ValueError(f"weight_decay must be >= 0 or None, got {weight_decay}")
+        _call(_lib.msa_cache8_attend, dev, stream, mem.handle,
+              _tensor(content, "content", (mem.n_chunks, 2, mem.n_kv_heads, mem.head_dim), mem.dtype,
+                      dev) if k else None,
+              _tensor(ids, "ids", (self.batch, k), torch.int32, dev) if k else None, k, self._ref,
+              T, H_q, _tensor(Q, "Q", shape, mem.dtype, dev), self._counts(n_tokens, "n_tokens"),
+              _tensor(O, "O", shape, mem.dtype, dev),
+              None if lse is None else _tensor(lse, "lse", shape[:3], torch.float32, dev),
+              -1.0 if weight_decay is None else weight_decay, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size())
+
+    def evict_workspace_size(self) -> int:
+        return _lib.msa_cache8_evict_workspace_size(self.mem.handle, self._ref)
+
+    def evict(self, budget: int, recent: int, workspace, out: "Cache8 | None" = None, stream=None):
+        """Keep at most ``budget`` rows a query: whole blocks leave by their accumulated attention
+        weight, the last ``recent`` rows' blocks stay (msa_cache8_evict); in place, or into
+        ``out``, a cache of the same batch, format and block_len."""
+        if out is None:
+            out = self
+        elif out.device != self.device or (out.mem.n_kv_heads, out.mem.head_dim) != (
+                self.mem.n_kv_heads, self.mem.head_dim):
+            raise ValueError("out must be on the same device and have the same head shapes")
+        _call(_lib.msa_cache8_evict, self.device, stream, self.mem.handle, self._ref, out._ref,
+              budget, recent, workspace.data_ptr(), workspace.numel() * workspace.element_size())
