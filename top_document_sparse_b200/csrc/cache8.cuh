@@ -426,7 +426,7 @@ cache8_move_kernel(EvictMove m, const int32_t *__restrict__ src_block,
   griddep_launch();
   const int64_t bh = blockIdx.y;
   const int b = blockIdx.y / m.H_kv, nb = m.cap / m.bl;
-  const int len = lens[2 * b], new_len = lens[2 * b + 1];
+  const int new_len = lens[2 * b + 1];
   const int32_t *src = src_block + bh * (nb + 1);
   const int pieces = m.bl * m.D / 16, wp = m.bl / 4;
   const int s = blockIdx.x * 128 + threadIdx.x;

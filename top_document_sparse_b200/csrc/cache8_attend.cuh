@@ -5,9 +5,9 @@
 //   weights_j = decay * weights_j + sum over tokens and heads of the group of p_j
 //
 // A few tokens: the bytes of the cache bound it.  Per (query, kv head, context
-// split) CTA, four warps each stream 16-row tiles straight from global memory
-// into the registers of mma.sync m16n8k16: no shared memory and no barrier
-// between tiles.  Context rows are the M rows of S^T = K Q^T and the K rows of
+// split) CTA, four warps each stream 16-row tiles through a ring of their own
+// (asynchronous copies, no barrier between warps) into mma.sync m16n8k16.
+// Context rows are the M rows of S^T = K Q^T and the K rows of
 // O^T += V^T P^T, the (token, head) columns the N columns, so no MMA row is
 // spent on a group's few heads.  The contraction index of an MMA may be
 // permuted freely: lane (g, t) = (lane / 4, lane % 4) reads 16-byte pieces t
@@ -29,12 +29,15 @@
 #pragma once
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "cache8.cuh"
 #include "context.cuh"
 
 namespace msa {
 
 constexpr int kC8Warps = 4;
+constexpr int kC8Stages = 3;          // tiles of a warp in flight or in use
 constexpr float kC8Shift = 11.0f;     // P is 2^11 exp2(s - m)
 constexpr float kC8Slack = 4.0f;      // a score may exceed m by this before m moves
 constexpr float kC8MinUnit = 0x1p-60f;  // smallest unit of O
@@ -47,16 +50,24 @@ struct Attend8Args {
   const uint8_t *k8, *v8;
   const float *ks, *vs;
   const int32_t *cache_len, *n_tokens;
-  int H_kv, G, T, cap, bl;
+  int H_kv, G, T, cap, bl, bl_shift;  // bl = 1 << bl_shift
+  uint32_t g_magic;                   // ceil(2^32 / G); 0 for G = 1
   const void *Q;
   float scale_log2;  // log2(e) / sqrt(D)
-  int n_split;
+  // context splits: the first loc_split share the local rows, the other n_split - loc_split the
+  // memory rows; with loc_split = n_split each takes a share of both
+  int n_split, loc_split;
   void *O;
   float *lse;
   float *part_o, *part_ml;
   float *weights;
   float decay;
 };
+
+// Token of a (token, head of the group) column: col / G, exact for col < 2^28.
+__device__ __forceinline__ int col_token(const Attend8Args &a, int col) {
+  return a.g_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(col), a.g_magic)) : col;
+}
 
 // Query b's tokens and rows; out-of-range lengths count as no tokens.
 struct Attend8Query {
@@ -109,54 +120,98 @@ __device__ __forceinline__ uint4 ld_stream16(const uint8_t *p) {
                : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint2 ld_stream8(const uint8_t *p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
-  return v;
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// A 16-row K tile of one head as this lane's bytes: words [row g or g + 8][D / 16].
+// A tile is 16 rows of K and of V of one head.  Each warp has a ring of its own in shared memory,
+// filled by 16-byte asynchronous copies; only the warp itself waits for them.  Within a row the
+// 16-byte pieces are permuted so that the fragment reads below hit every bank once (D = 128; at
+// D = 64 V's reads are two to a bank).
+template <int D>
+struct Tile8 {
+  static constexpr int kRow = D, kBytes = 16 * D, kStage = 2 * kBytes;
+  static __device__ __forceinline__ uint32_t k_off(int row, int piece) {
+    return row * D + ((D == 128 ? piece ^ ((row & 1) << 2) : piece) << 4);
+  }
+  static __device__ __forceinline__ uint32_t v_off(int row, int piece) {
+    return row * D + ((D == 128 ? piece ^ (row & 6) : piece ^ ((row >> 1) & 3)) << 4);
+  }
+  // the warp's copies of the tile whose rows start at k and v
+  static __device__ __forceinline__ void issue(uint32_t stage, const uint8_t *k, const uint8_t *v,
+                                               int lane) {
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      const int i = lane + 32 * u, row = i / (D / 16), piece = i % (D / 16);
+      cp_async_16(stage + k_off(row, piece), k + 16 * i, true);
+      cp_async_16(stage + kBytes + v_off(row, piece), v + 16 * i, true);
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// This lane's bytes of a K tile: words [row g or g + 8][D / 16].
 template <int D>
 struct KTile {
   uint32_t w[2][D / 16];
-  // rows >= lim read as zero
-  __device__ __forceinline__ void load(const uint8_t *tile, int lane, int lim) {
+  __device__ __forceinline__ void set(int r, int p, uint4 x) {
+    w[r][4 * p] = x.x; w[r][4 * p + 1] = x.y; w[r][4 * p + 2] = x.z; w[r][4 * p + 3] = x.w;
+  }
+  __device__ __forceinline__ void from_shared(uint32_t stage, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int p = 0; p < D / 64; ++p) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (g + 8 * r < lim) x = ld_stream16(tile + (g + 8 * r) * D + 64 * p + 16 * t);
-        w[r][4 * p] = x.x; w[r][4 * p + 1] = x.y; w[r][4 * p + 2] = x.z; w[r][4 * p + 3] = x.w;
-      }
+      for (int p = 0; p < D / 64; ++p) set(r, p, lds16(stage + Tile8<D>::k_off(g + 8 * r, 4 * p + t)));
+  }
+  __device__ __forceinline__ void from_global(const uint8_t *tile, int lane) {
+    const uint8_t *x = tile + (lane >> 2) * D + 16 * (lane & 3);
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int p = 0; p < D / 64; ++p) set(r, p, ld_stream16(x + 8 * r * D + 64 * p));
   }
 };
-// A 16-row V tile: words [row 2t, 2t + 1, 2t + 8, 2t + 9][D / 32] of bytes (D / 8) g ...
+
+// This lane's bytes of a V tile: words [row 2t, 2t + 1, 2t + 8, 2t + 9][D / 32] from byte (D / 8) g.
 template <int D>
 struct VTile {
   uint32_t w[4][D / 32];
-  __device__ __forceinline__ void load(const uint8_t *tile, int lane, int lim) {
+  __device__ __forceinline__ void from_shared(uint32_t stage, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 2 * t + (r & 1) + 8 * (r >> 1);
       if constexpr (D == 128) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < lim) x = ld_stream16(tile + row * D + 16 * g);
+        const uint4 x = lds16(stage + Tile8<D>::v_off(row, g));
         w[r][0] = x.x; w[r][1] = x.y; w[r][2] = x.z; w[r][3] = x.w;
       } else {
-        uint2 x = make_uint2(0, 0);
-        if (row < lim) x = ld_stream8(tile + row * D + 8 * g);
+        const uint2 x = lds8(stage + Tile8<D>::v_off(row, g >> 1) + 8 * (g & 1));
         w[r][0] = x.x; w[r][1] = x.y;
       }
     }
+  }
+  // rows >= lim become zero: a byte behind the last row may be e4m3's NaN, and 0 * NaN is NaN
+  __device__ __forceinline__ void clear_from(int lane, int lim) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (2 * (lane & 3) + (r & 1) + 8 * (r >> 1) >= lim) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) w[r][i] = 0;
+      }
   }
 };
 
@@ -172,8 +227,11 @@ struct Attend8Smem {
   static constexpr int kQb = kQ + kCols * kQPitch * 2;           // bf16, as given
   static constexpr int kColScale = kQb + kCols * kQPitch * 2;    // fp32 per column
   static constexpr int kMerge = kColScale + kCols * 4;
-  static constexpr int kMergeBytes = kC8Warps * kCols * (D + 4) * 4;  // O, m, l, unit
-  static constexpr int kTable = kMerge + kMergeBytes;            // prefix, bases, chunk table
+  static constexpr int kMergeBytes = kC8Warps * kCols * (D + 4) * 4;  // O, m, l
+  static constexpr int kRing = kMerge;                           // the rings, before the merge
+  static constexpr int kRingBytes = kC8Warps * kC8Stages * Tile8<D>::kStage;
+  static constexpr int kTable = kMerge + (kMergeBytes > kRingBytes ? kMergeBytes : kRingBytes);
+  // prefix, bases, chunk table
   static int bytes(int table_cap) { return kTable + (2 * kMaxTopK + 1 + table_cap) * 4; }
 };
 
@@ -189,32 +247,31 @@ __device__ __forceinline__ void load_q_columns(const Attend8Args &a, int b, int 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   constexpr int E = D / 32;
   for (int c = warp; c < Sm::kCols; c += kC8Warps) {
-    const int cc = c0 + c, t = cc / a.G;
-    __nv_bfloat16 x[E];
-    float amax = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = __float2bfloat16_rn(0.0f);
-    if (t < n) {
-      const __nv_bfloat16 *row =
+    const int cc = c0 + c, t = col_token(a, cc);
+    using Raw = std::conditional_t<E == 4, uint2, uint32_t>;  // this lane's elements
+    Raw raw{};
+    if (t < n)
+      raw = *reinterpret_cast<const Raw *>(
           static_cast<const __nv_bfloat16 *>(a.Q) +
-          ((static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc % a.G) * D + lane * E;
-      if constexpr (E == 4)
-        *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(row);
-      else
-        *reinterpret_cast<uint32_t *>(x) = *reinterpret_cast<const uint32_t *>(row);
-    }
+          ((static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc - t * a.G) * D + lane * E);
+    uint32_t w[E / 2], h[E / 2];
+    *reinterpret_cast<Raw *>(w) = raw;
+    float x[E], amax = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) amax = fmaxf(amax, finite_abs(__bfloat162float(x[e])));
+    for (int e = 0; e < E; e += 2) {
+      x[e] = __uint_as_float(w[e / 2] << 16);
+      x[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
+      amax = fmaxf(amax, fmaxf(finite_abs(x[e]), finite_abs(x[e + 1])));
+    }
     amax = warp_max(amax);
-    int ex = 0;
-    if (amax > 0.0f) ex = max(-126, min(126, ilogbf(amax)));
-    const float inv = ldexpf(1.0f, -ex);
+    // 2^ex <= amax < 2^(ex + 1), within [-126, 126] so that 2^-ex is a normal number too
+    const int ex = amax == 0.0f ? 0 : max(1, min(253, __float_as_int(amax) >> 23)) - 127;
+    const float inv = __int_as_float((127 - ex) << 23);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      qb[c * Sm::kQPitch + lane * E + e] = x[e];
-      qh[c * Sm::kQPitch + lane * E + e] = __float2half_rn(__bfloat162float(x[e]) * inv);
-    }
-    if (lane == 0) cs[c] = ldexpf(a.scale_log2, ex);
+    for (int e = 0; e < E; e += 2) h[e / 2] = pack_f16x2(x[e] * inv, x[e + 1] * inv);
+    *reinterpret_cast<Raw *>(qb + c * Sm::kQPitch + lane * E) = raw;
+    *reinterpret_cast<Raw *>(qh + c * Sm::kQPitch + lane * E) = *reinterpret_cast<Raw *>(h);
+    if (lane == 0) cs[c] = a.scale_log2 * __int_as_float((127 + ex) << 23);
   }
 }
 
@@ -224,10 +281,11 @@ template <int D, int NT>
 struct Softmax8 {
   float m[NT][2], l[NT][2];
   float acc[NT][D / 16][4];  // O^T, [d pair][col pair], in units of `unit`
-  float unit;
+  float unit, inv_unit;  // a power of two and its reciprocal, the same in every lane
 
   __device__ __forceinline__ void init() {
     unit = kC8MinUnit;
+    inv_unit = 1.0f / kC8MinUnit;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
@@ -240,9 +298,10 @@ struct Softmax8 {
   }
   // O's unit becomes at least v
   __device__ __forceinline__ void raise_unit(float v) {
-    if (v > unit) {  // the same in every lane
+    if (v > unit) {
       const float f = unit / v;
       unit = v;
+      inv_unit = 1.0f / v;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -292,9 +351,14 @@ struct Softmax8 {
   }
 };
 
+// Start of part i of n tiles cut into `parts`.
+__device__ __forceinline__ int share(int n, int i, int parts) {
+  return static_cast<int>(static_cast<int64_t>(n) * i / parts);
+}
+
 // Rows a column sees: row of its token plus one.
 __device__ __forceinline__ int column_rows(const Attend8Args &a, const Attend8Query &q, int col) {
-  const int t = col / a.G;
+  const int t = col_token(a, col);
   return t < q.n ? q.len - q.n + t + 1 : 0;
 }
 
@@ -303,9 +367,9 @@ __device__ __forceinline__ int column_rows(const Attend8Args &a, const Attend8Qu
 template <typename T, int D, int COLS>
 __device__ __forceinline__ void merge_warps(const Attend8Args &a, const Attend8Query &q, int b,
                                             int g, int c0, int split, const float *merge) {
-  for (int i = threadIdx.x; i < COLS * D; i += 32 * kC8Warps) {
-    const int c = i / D, d = i % D, cc = c0 + c, t = cc / a.G;
-    if (t >= q.n) continue;
+  const int cols = min(COLS, q.n * a.G - c0);
+  for (int i = threadIdx.x; i < cols * D; i += 32 * kC8Warps) {
+    const int c = i / D, d = i % D, cc = c0 + c, t = col_token(a, cc);
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kC8Warps; ++w) M = fmaxf(M, merge[(w * COLS + c) * (D + 4) + D]);
@@ -314,11 +378,11 @@ __device__ __forceinline__ void merge_warps(const Attend8Args &a, const Attend8Q
 #pragma unroll
     for (int w = 0; w < kC8Warps; ++w) {
       const float *row = merge + (w * COLS + c) * (D + 4);
-      const float f = exp2f(row[D] - base);
+      const float f = ex2_approx(row[D] - base);
       L += row[D + 1] * f;
       o += row[d] * f;
     }
-    const int64_t row = (static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc % a.G;
+    const int64_t row = (static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc - t * a.G;
     if (a.n_split == 1) {
       static_cast<T *>(a.O)[row * D + d] = Elem<T>::from_f(L == 0.0f ? 0.0f : o / L);
       if (d == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
@@ -334,7 +398,7 @@ __device__ __forceinline__ void merge_warps(const Attend8Args &a, const Attend8Q
 
 // grid (B * H_kv, n_split, column tiles), block 32 * kC8Warps.
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(32 * kC8Warps)
+__global__ void __launch_bounds__(32 * kC8Warps, NT == 1 ? 4 : NT == 2 ? 3 : 2)
 cache8_attend_kernel(Attend8Args a) {
   using Sm = Attend8Smem<D, NT>;
   constexpr int KS = D / 16;  // k steps of S^T
@@ -347,33 +411,40 @@ cache8_attend_kernel(Attend8Args a) {
   griddep_launch();
   const Attend8Query q = attend8_query(a, b, blockIdx.x % a.H_kv == 0 && split == 0 && c0 == 0 &&
                                                  threadIdx.x == 0);
-  if (c0 / a.G >= q.n) return;  // padding tokens only (the whole CTA)
+  if (col_token(a, c0) >= q.n) return;  // padding tokens only (the whole CTA)
   const int last_col = min(c0 + Sm::kCols, q.n * a.G) - 1;
   const int n_loc = max(0, column_rows(a, q, last_col));  // rows any column sees
   const int all_see = column_rows(a, q, c0);              // rows every real column sees
+  const bool own_mem = a.loc_split < a.n_split;  // memory rows have splits of their own
   const int nl = (n_loc + 15) / 16;
-  const int l0 = static_cast<int>(static_cast<int64_t>(nl) * split / a.n_split);
-  const int l1 = static_cast<int>(static_cast<int64_t>(nl) * (split + 1) / a.n_split);
+  const int l0 = split < a.loc_split ? share(nl, split, a.loc_split) : 0;
+  const int l1 = split < a.loc_split ? share(nl, split + 1, a.loc_split) : 0;
   const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
-  const uint8_t *kbase = a.k8 + bh * a.cap * D, *vbase = a.v8 + bh * a.cap * D;
-  const float *ks = a.ks + bh * (a.cap / a.bl), *vs = a.vs + bh * (a.cap / a.bl);
+  const float *ks = a.ks + bh * (a.cap >> a.bl_shift), *vs = a.vs + bh * (a.cap >> a.bl_shift);
 
-  // the first tile is in flight while Q and the chunk table are set up
-  KTile<D> kt;
-  VTile<D> vt;
+  // the first tiles are in flight while Q and the chunk table are set up
+  int tile = l0 + warp, ahead = tile;  // the tile in use, the next one to fetch
+  const uint8_t *kp = a.k8 + (bh * a.cap + tile * 16) * D, *vp = a.v8 + (bh * a.cap + tile * 16) * D;
+  const uint32_t ring = smem_u32(sm + Sm::kRing) + warp * kC8Stages * Tile8<D>::kStage;
+  auto fetch = [&](uint32_t stage) {
+    if (ahead < l1) Tile8<D>::issue(stage, kp, vp, lane);
+    cp_async_commit();  // an empty group too: the count of groups is the count of tiles
+    ahead += kC8Warps;
+    kp += kC8Warps * 16 * D;
+    vp += kC8Warps * 16 * D;
+  };
+#pragma unroll
+  for (int i = 0; i < kC8Stages - 1; ++i) fetch(ring + i * Tile8<D>::kStage);
   float ksc = 0.0f, vsc = 0.0f;
-  int tile = l0 + warp;
   if (tile < l1) {
-    kt.load(kbase + static_cast<int64_t>(tile) * 16 * D, lane, n_loc - tile * 16);
-    vt.load(vbase + static_cast<int64_t>(tile) * 16 * D, lane, n_loc - tile * 16);
-    ksc = ks[tile * 16 / a.bl];
-    vsc = vs[tile * 16 / a.bl];
+    ksc = ks[(tile * 16) >> a.bl_shift];
+    vsc = vs[(tile * 16) >> a.bl_shift];
   }
   load_q_columns<D, NT>(a, b, g, c0, q.n, sm);
   int *pre = reinterpret_cast<int *>(sm + Sm::kTable), *base = pre + kMaxTopK + 1;
   int *table = base + kMaxTopK;
   int n_mem = 0;
-  if (a.k > 0)
+  if (a.k > 0 && (!own_mem || split >= a.loc_split))
     n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
                               nullptr, 0, table, pre, base, a.table_cap);
   __syncthreads();
@@ -404,8 +475,16 @@ cache8_attend_kernel(Attend8Args a) {
   st.init();
 
   // ---- local rows
+  int stage = 0;
   for (; tile < l1; tile += kC8Warps) {
     const int next = tile + kC8Warps;
+    cp_async_wait<kC8Stages - 2>();
+    __syncwarp();  // every lane's copies of this tile are there; the last tile's stage is free
+    const uint32_t at = ring + stage * Tile8<D>::kStage;
+    fetch(ring + (stage == 0 ? kC8Stages - 1 : stage - 1) * Tile8<D>::kStage);
+    stage = stage == kC8Stages - 1 ? 0 : stage + 1;
+    KTile<D> kt;
+    kt.from_shared(at, lane);
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -427,10 +506,9 @@ cache8_attend_kernel(Attend8Args a) {
       }
     }
     const float k_scale = ksc, v_scale = vsc;
-    if (next < l1) {  // K's registers are free: the next tile's
-      kt.load(kbase + static_cast<int64_t>(next) * 16 * D, lane, n_loc - next * 16);
-      ksc = ks[next * 16 / a.bl];
-      vsc = vs[next * 16 / a.bl];
+    if (next < l1) {
+      ksc = ks[(next * 16) >> a.bl_shift];
+      vsc = vs[(next * 16) >> a.bl_shift];
     }
     const int x0 = tile * 16;
 #pragma unroll
@@ -446,13 +524,16 @@ cache8_attend_kernel(Attend8Args a) {
     }
     st.step(s);
     st.raise_unit(v_scale);
-    const float ratio = v_scale / st.unit;
+    const float ratio = v_scale * st.inv_unit;
     uint32_t pb[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       pb[nt][0] = movmatrix_trans(pack_f16x2(s[nt][0] * ratio, s[nt][1] * ratio));
       pb[nt][1] = movmatrix_trans(pack_f16x2(s[nt][2] * ratio, s[nt][3] * ratio));
     }
+    VTile<D> vt;
+    vt.from_shared(at + Tile8<D>::kBytes, lane);
+    if (FMT == MSA_CACHE_E4M3 && x0 + 16 > n_loc) vt.clear_from(lane, n_loc - x0);
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
       // words w of four rows: elements (D / 8) g + 4 w .. + 3, two M tiles
@@ -471,17 +552,16 @@ cache8_attend_kernel(Attend8Args a) {
           mma_f16_16816(st.acc[nt][2 * w + i], lo[0][i], hi[0][i], lo[1][i], hi[1][i], pb[nt][0],
                         pb[nt][1]);
     }
-    if (next < l1) vt.load(vbase + static_cast<int64_t>(next) * 16 * D, lane, n_loc - next * 16);
   }
 
   // ---- memory rows: every column sees them
   const int nm = (n_mem + 15) / 16;
-  const int m1 = static_cast<int>(static_cast<int64_t>(nm) * (split + 1) / a.n_split);
+  const int ms = own_mem ? split - a.loc_split : split, mn = own_mem ? a.n_split - a.loc_split : a.n_split;
+  const int m1 = share(nm, ms + 1, mn);
   const __nv_bfloat16 *qb = reinterpret_cast<const __nv_bfloat16 *>(sm + Sm::kQb);
   const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
-  const float to_unit = 1.0f / st.unit;
-  for (int mt = static_cast<int>(static_cast<int64_t>(nm) * split / a.n_split) + warp; mt < m1;
-       mt += kC8Warps) {
+  const float to_unit = st.inv_unit;
+  for (int mt = share(nm, ms, mn) + warp; mt < m1; mt += kC8Warps) {
     const int x0 = mt * 16;
     auto row_ptr = [&](int x) {
       return static_cast<const __nv_bfloat16 *>(a.content) +
@@ -513,9 +593,7 @@ cache8_attend_kernel(Attend8Args a) {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int t = (c0 + 8 * nt + 2 * lt + (e & 1)) / a.G;
-        const bool ok = x0 + lg + 8 * (e >> 1) < n_mem && t < q.n;
-        s[nt][e] = ok ? s[nt][e] * a.scale_log2 : -INFINITY;
+        s[nt][e] = x0 + lg + 8 * (e >> 1) < n_mem ? s[nt][e] * a.scale_log2 : -INFINITY;
       }
     st.step(s);
     uint32_t pb[NT][2][2];  // [part][row half]
@@ -551,6 +629,8 @@ cache8_attend_kernel(Attend8Args a) {
   }
 
   // ---- the warps meet
+  cp_async_wait<0>();
+  __syncthreads();  // every warp is done with its ring
   float *merge = reinterpret_cast<float *>(sm + Sm::kMerge);
   const float out = st.unit * exp2f(-kC8Shift);
 #pragma unroll
@@ -618,7 +698,7 @@ cache8_attend_f32_kernel(Attend8Args a) {
   __syncthreads();
   const int last_col = min(c0 + C, q.n * a.G) - 1;
   const int n_loc = max(0, column_rows(a, q, last_col));
-  const int nl = (n_loc + 31) / 32, nm = (n_mem + 31) / 32, n = nl + nm;
+  const int nl = (n_loc + 31) / 32, nm = (n_mem + 31) / 32, n = nl + nm;  // shares of both
   const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
   const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
   int rows[C];
@@ -632,9 +712,8 @@ cache8_attend_f32_kernel(Attend8Args a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[c][e] = 0.0f;
   }
-  const int i1 = static_cast<int>(static_cast<int64_t>(n) * (split + 1) / a.n_split);
-  for (int i = static_cast<int>(static_cast<int64_t>(n) * split / a.n_split) + warp; i < i1;
-       i += kC8Warps) {
+  const int i1 = share(n, split + 1, a.n_split);
+  for (int i = share(n, split, a.n_split) + warp; i < i1; i += kC8Warps) {
     const bool loc = i < nl;
     const int x0 = (loc ? i : i - nl) * 32, x = x0 + lane;
     const int lim = loc ? n_loc : n_mem;
@@ -775,8 +854,8 @@ cache8_weight_kernel(Attend8Args a) {
   float k_scale = 0.0f;
   if (work) {
     KTile<D> kt;
-    kt.load(a.k8 + (bh * a.cap + x0) * D, lane, q.len - x0);
-    k_scale = a.ks[bh * (a.cap / a.bl) + x0 / a.bl];
+    kt.from_global(a.k8 + (bh * a.cap + x0) * D, lane);
+    k_scale = a.ks[(bh * a.cap + x0) >> a.bl_shift];
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       widen4<FMT>(kt.w[0][i], ka[i][0], ka[i][2]);
@@ -790,10 +869,10 @@ cache8_weight_kernel(Attend8Args a) {
     if (c0) __syncthreads();
     load_q_columns<D, NT>(a, b, g, c0, q.n, sm);
     for (int c = threadIdx.x; c < Sm::kCols; c += 32 * kC8Warps) {
-      const int cc = c0 + c, t = cc / a.G;
+      const int cc = c0 + c, t = col_token(a, cc);
       float v = INFINITY;  // no token, or one that sees nothing: weight 0
       if (t < q.n) {
-        const float x = a.lse[(static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc % a.G];
+        const float x = a.lse[(static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc - t * a.G];
         if (x != -INFINITY) v = x * kLog2e;
       }
       lse2[c] = v;

@@ -183,7 +183,7 @@ msa_status dispatch8(const msa_memory *mem, int format, F &&f) {
 int attend8_nt(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 
 struct Attend8Plan {
-  int n_split = 1, col_tiles = 1, table_cap = 0;
+  int n_split = 1, loc_split = 1, col_tiles = 1, table_cap = 0;
   size_t part_o = 0, part_ml = 0, lse = 0, bytes = 0;
 };
 
@@ -197,9 +197,17 @@ Attend8Plan plan_attend8(const msa_memory *mem, const msa_cache8 *c, int T, int 
   p.col_tiles = static_cast<int>((cols + per - 1) / per);
   const int64_t ctas = static_cast<int64_t>(c->batch) * mem->H_kv * p.col_tiles;
   const int64_t want = 3LL * num_sms();
-  if (ctas < want) {
-    const int64_t by_len = std::max<int64_t>(1, (static_cast<int64_t>(c->capacity) + max_mem + 63) / 64);
-    p.n_split = static_cast<int>(std::min<int64_t>(std::min<int64_t>((want + ctas - 1) / ctas, by_len), 64));
+  // Splits of at most 2,048 local rows, so that ragged lengths spread over the SMs, and enough of
+  // them for three CTAs an SM (64 queries of up to 8,192 rows: 133 us at 4,096 rows a split, 124
+  // at 2,048, 131 at 1,024).  Where the context is split anyway, the memory rows get splits of
+  // their own, so that the others need no chunk table.
+  int64_t loc = (c->capacity + 2047) / 2048;
+  if (ctas * loc < want) loc = std::min<int64_t>((want + ctas - 1) / ctas, (c->capacity + 63) / 64);
+  loc = std::min<int64_t>(loc, 64);
+  p.n_split = p.loc_split = static_cast<int>(loc);
+  if (mem->dtype == MSA_BF16 && max_mem > 0 && (loc > 1 || ctas < want)) {
+    const int64_t own = std::min<int64_t>((max_mem + 63) / 64, std::max<int64_t>(1, want / ctas));
+    p.n_split += static_cast<int>(std::min<int64_t>(own, 64));
   }
   const size_t rows = static_cast<size_t>(c->batch) * T * H_q;
   if (p.n_split > 1) {
@@ -459,12 +467,15 @@ msa_status msa_cache8_attend(const msa_memory *mem, const void *content, const i
   a.n_tokens = n_tokens;
   a.H_kv = mem->H_kv;
   a.G = n_q_heads / mem->H_kv;
+  a.g_magic = a.G == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + a.G - 1) / a.G);
   a.T = tokens;
   a.cap = cache->capacity;
   a.bl = cache->block_len;
+  a.bl_shift = cache->block_len == 16 ? 4 : cache->block_len == 32 ? 5 : cache->block_len == 64 ? 6 : 7;
   a.Q = Q;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(mem->D)));
   a.n_split = p.n_split;
+  a.loc_split = p.loc_split;
   a.O = O;
   a.lse = lse ? lse : track ? reinterpret_cast<float *>(ws + p.lse) : nullptr;
   a.part_o = reinterpret_cast<float *>(ws + p.part_o);
