@@ -21,9 +21,9 @@
 // int8 -> fp16 is a byte permute that sets the bits of 1024 + (q + 128) and
 // one subtraction.  Q is scaled by a power of two per column to 1 <= max|q| < 2, which loses
 // nothing of a bf16 row down to 2^-17 of its largest element.  P is kept at
-// 2^11 times its size against a reference maximum that moves only when a score
-// exceeds it by 4 (log2 units): at most 2^15, and rows down to 2^-25 of the
-// largest keep fp16's full 11 bits.
+// 2^11 times its size against a reference that moves, to 4 above the score (log2
+// units), only when a score exceeds it by 4: at most 2^15, and weights down to
+// 2^-21 of the largest keep fp16's full 11 bits.
 //   Memory rows are bf16 and go through bf16 MMAs; P is split there into a bf16
 // head and tail, two MMAs, so it loses nothing either.
 #pragma once
@@ -39,7 +39,8 @@ namespace msa {
 constexpr int kC8Warps = 4;
 constexpr int kC8Stages = 3;          // tiles of a warp in flight or in use
 constexpr float kC8Shift = 11.0f;     // P is 2^11 exp2(s - m)
-constexpr float kC8Slack = 4.0f;      // a score may exceed m by this before m moves
+constexpr float kC8Slack = 4.0f;      // a score may exceed m by this before m moves,
+constexpr float kC8Lead = 4.0f;       // and m then moves this far above it
 constexpr float kC8MinUnit = 0x1p-60f;  // smallest unit of O
 
 struct Attend8Args {
@@ -327,8 +328,8 @@ struct Softmax8 {
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          const float mn = fmaxf(m[nt][h], v);
-          const float f = mn == -INFINITY ? 1.0f : ex2_approx(m[nt][h] - mn);
+          const float mn = v > m[nt][h] + kC8Slack ? v + kC8Lead : m[nt][h];
+          const float f = mn == m[nt][h] ? 1.0f : ex2_approx(m[nt][h] - mn);
           m[nt][h] = mn;
           l[nt][h] *= f;
 #pragma unroll

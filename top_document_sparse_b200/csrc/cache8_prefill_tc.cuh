@@ -1,0 +1,573 @@
+// cache8_prefill_tc.cuh -- attention of many new tokens over [8-bit local rows
+// | retrieved memory rows] on the 5th-generation tensor cores: the arithmetic
+// of cache8_attend.cuh (4 D FLOP for every visible (row, column) pair), which
+// bounds it once a context row is shared by some hundred columns.
+//
+// One CTA per (query, kv head, pair of tiles of 128 columns, context split); a
+// column is a (token, head of the group) pair and owns one TMEM lane and one
+// softmax thread.  Both tiles share every context block of 64 rows:
+//   converters (warps 10-13) load a block's bytes, widen them to fp16 in
+//        registers and write them to shared memory in the MMA's layout, K and V
+//        each into a ring of four.  A block that spans several cache scales is
+//        brought to the largest of them by an exact power of two in the widening
+//        FMA, so one scale for K and one for V leave with the block.  bf16
+//        memory rows are brought to fp16 the same way, by a power of two that
+//        takes the block's largest element below 2.
+//   warps 8, 9  one for each tile: a thread issues S = Q K^T (M 128, N 64, K D; Q fp16, scaled by a
+//        power of two per column) into one of two TMEM buffers a tile, and
+//        O += P V (M 128, N D, K 64), each as soon as its inputs are ready (one
+//        warp for both tiles was bound by the issue: 72 cycles an MMA, 113 a
+//        commit, 120 a barrier test)
+//   warps 0-3, 4-7  the softmax of a tile, a thread a column: S from TMEM, the
+//        hidden rows masked, P = 2^11 2^(s - m) times V's scale over the unit of
+//        O, written as fp16 over S: P is the MMA's A operand straight from TMEM,
+//        so nothing but Q, K and V passes through shared memory.  The softmax of
+//        a block waits for no P V: the next S is ready when it ends, and only a
+//        move of the reference m (when a score passes it by 4 in log2 units; to 4
+//        above the score) waits for O's last update and rescales O's lane.  The
+//        ratio of V's scale to the unit is a whole power of two and goes into the
+//        exponent; the sum of a block's weights is brought back by the same power.
+// 512 tokens x 32 heads over 8,704 + 128 rows: 166 us with P through shared
+// memory, 153 with blocks of 128 rows and one S a tile (S, softmax and P V of a
+// tile then follow one another).
+// Every wait is bounded: on timeout the CTA raises MSA_DEVERR_WAIT_TIMEOUT,
+// every role skips the rest (the outputs are then void), and issued MMAs are
+// drained before TMEM is freed.
+#pragma once
+#include "cache8_attend.cuh"
+#include "tc05.cuh"
+
+namespace msa {
+
+constexpr int kC8tConv = 128;                       // converter threads
+constexpr int kC8tThreads = 32 * 10 + kC8tConv;
+constexpr int kC8tBlk = 64;                         // context rows per block
+constexpr int kC8tSlots = 4;                        // ring of K, ring of V
+constexpr int kC8tRows = 128;                       // columns per tile (UMMA M)
+constexpr uint32_t kC8tTmemCols = 512;              // S, then P, of tile x at 128 x + 64 (block % 2),
+constexpr uint32_t kC8tTmemO = 256;                 // O of tile x at 256 + 128 x
+
+enum {
+  kCbFullK0 = 0,                       // K slot holds its block (every converter thread)
+  kCbFullV0 = kCbFullK0 + kC8tSlots,   // V slot
+  kCbFreeK0 = kCbFullV0 + kC8tSlots,   // every Q K^T reading the slot completed (commit)
+  kCbFreeV0 = kCbFreeK0 + kC8tSlots,   // every P V reading the slot completed (commit)
+  kCbS0 = kCbFreeV0 + kC8tSlots,       // S buffer (tile, block % 2) computed (commit) [4]
+  kCbO0 = kCbS0 + 4,                   // P V of (tile, block % 2) completed (commit) [4]
+  kCbQ0 = kCbO0 + 4,                   // tile's Q in shared memory (128 threads) [2]
+  kCbP0 = kCbQ0 + 2,                   // P of (tile, block % 2) written, O rescaled (128 threads) [4];
+                                       // one for each buffer: a softmax may be a block ahead of P V
+  kCbDrain = kCbP0 + 4,                // a tile's MMAs all completed (commit) [2]
+  kCbN = kCbDrain + 2
+};
+
+struct C8tSmem {
+  static constexpr int D = 128;
+  static constexpr int kQBytes = 2 * kC8tRows * 128;    // [panel][128 rows][128 B]
+  static constexpr int kKVBytes = 2 * kC8tBlk * 128;    // [panel][64 rows][128 B]
+  static constexpr int kK = 2 * kQBytes;                // slots
+  static constexpr int kV = kK + kC8tSlots * kKVBytes;
+  static constexpr int kBars = kV + kC8tSlots * kKVBytes;
+  static constexpr int kScale = kBars + kCbN * 8;       // [block % (2 slots)][K, V]
+  static constexpr int kRed = kScale + 2 * kC8tSlots * 8;  // [converter warp]
+  static constexpr int kMisc = kRed + 16;               // TMEM slot, fail
+  static constexpr int kPre = kMisc + 16;
+  static int bytes(int table_cap) { return 1024 + kPre + (2 * kMaxTopK + 1 + table_cap) * 4; }
+};
+
+// Instruction descriptor, kind::f16: fp16 A and B, fp32 D.
+template <int M, int N>
+__host__ __device__ constexpr uint32_t umma_idesc_f16_f32() {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The same MMA with A in TMEM (a lane a row, two fp16 of K a column).
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Store 32 consecutive columns of this thread's TMEM lane, then wait for the store.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};\n"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+      "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+// Load 32 consecutive columns of this thread's TMEM lane and wait for them.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four cached values as two fp16 pairs, times f (a power of two <= 1).
+template <int FMT>
+__device__ __forceinline__ uint2 widen4_scaled(uint32_t w, __half2 f, __half2 bias) {
+  uint32_t lo, hi;
+  if constexpr (FMT == MSA_CACHE_INT8) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 a = __hfma2(*reinterpret_cast<const __half2 *>(&x), f, bias);  // (1152 + q) f - 1152 f
+    const __half2 b = __hfma2(*reinterpret_cast<const __half2 *>(&y), f, bias);
+    lo = *reinterpret_cast<const uint32_t *>(&a);
+    hi = *reinterpret_cast<const uint32_t *>(&b);
+  } else {
+    widen4<FMT>(w, lo, hi);
+    const __half2 a = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f);
+    const __half2 b = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f);
+    lo = *reinterpret_cast<const uint32_t *>(&a);
+    hi = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  return make_uint2(lo, hi);
+}
+
+// The power of two at or below a finite x > 0, within the normal numbers that have a reciprocal.
+__device__ __forceinline__ float floor_pow2(float x) {
+  return __int_as_float(max(1, min(253, __float_as_int(x) >> 23)) << 23);
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// grid (pairs * B * H_kv, n_split), block kC8tThreads, one CTA per SM.
+template <int FMT>
+__global__ void __launch_bounds__(kC8tThreads, 1)
+cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
+  using Sm = C8tSmem;
+  constexpr int D = 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Sm::kBars);
+  float *scales = reinterpret_cast<float *>(sm + Sm::kScale);
+  float *red = reinterpret_cast<float *>(sm + Sm::kRed);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Sm::kMisc);
+  volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  int *pre = reinterpret_cast<int *>(sm + Sm::kPre), *base = pre + kMaxTopK + 1;
+  int *table = base + kMaxTopK;
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+
+  const int bg = static_cast<int>(blockIdx.x / n_pairs), b = bg / a.H_kv, g = bg % a.H_kv;
+  const int pair = n_pairs - 1 - static_cast<int>(blockIdx.x % n_pairs);  // most context first
+  const int split = blockIdx.y;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  griddep_wait();
+  griddep_launch();
+  const Attend8Query q = attend8_query(a, b, pair == 0 && g == 0 && split == 0 && threadIdx.x == 0);
+  const int cols = q.n * a.G;  // real columns of this (query, kv head)
+  const int c0 = pair * 2 * kC8tRows;
+  if (c0 >= cols) return;  // padding tokens only (the whole CTA)
+  const bool act1 = c0 + kC8tRows < cols;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kC8tSlots; ++i) {
+      mbar_init(bar(kCbFullK0 + i), kC8tConv);
+      mbar_init(bar(kCbFullV0 + i), kC8tConv);
+      mbar_init(bar(kCbFreeK0 + i), act1 ? 2 : 1);  // one commit a tile
+      mbar_init(bar(kCbFreeV0 + i), act1 ? 2 : 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(kCbS0 + i), 1);
+      mbar_init(bar(kCbO0 + i), 1);
+      mbar_init(bar(kCbP0 + i), 128);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(bar(kCbQ0 + i), 128);
+    mbar_init(bar(kCbDrain), 1);
+    mbar_init(bar(kCbDrain + 1), 1);
+    *fail = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(smem_u32(tmem_slot), kC8tTmemCols);
+  int n_mem = 0;
+  if (a.k > 0)
+    n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
+                              nullptr, 0, table, pre, base, a.table_cap);
+  tc05_fence_before();
+  __syncthreads();  // barriers, the fail flag and the TMEM address are visible
+  tc05_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // this split's blocks: of the local ones [0, lb) and the memory ones behind them
+  const int n_loc = max(0, column_rows(a, q, min(c0 + 2 * kC8tRows, cols) - 1));
+  const int lb = (n_loc + kC8tBlk - 1) / kC8tBlk, mb = (n_mem + kC8tBlk - 1) / kC8tBlk;
+  const int u0 = share(lb + mb, split, a.n_split), u1 = share(lb + mb, split + 1, a.n_split);
+  const int nblk = u1 - u0;
+  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
+
+  // bounded wait; false (and every later wait false at once) after a timeout anywhere
+  auto wait = [&](int i, uint32_t parity) -> bool {
+    if (*fail) return false;
+    if (mbar_wait(bar(i), parity)) return true;
+    *fail = 1;
+    raise_device_error(MSA_DEVERR_WAIT_TIMEOUT);
+    return false;
+  };
+
+  if (warp >= 10) {
+    // ------------------------------------------------------------ converters
+    const int tid = threadIdx.x - 32 * 10;
+    // after a timeout the loops run on without work, so that every converter thread reaches the
+    // memory blocks' barriers
+    bool live = true;
+    // half h (0: K, 1: V) of the j-th block: its slot, waited for; false after a timeout
+    auto slot = [&](int j, int h) { return sm + (h ? Sm::kV : Sm::kK) + (j % kC8tSlots) * Sm::kKVBytes; };
+    auto wait_slot = [&](int j, int h) {
+      if (j >= kC8tSlots)
+        live = live && wait((h ? kCbFreeV0 : kCbFreeK0) + j % kC8tSlots, (j / kC8tSlots - 1) & 1);
+      return live;
+    };
+    auto landed = [&](int j, int h) {
+      fence_proxy_async_smem();  // the rows become visible to the tensor cores
+      mbar_arrive(bar((h ? kCbFullV0 : kCbFullK0) + j % kC8tSlots));
+    };
+    // Local rows.  Piece i of a thread lies in rows 16 i .. 16 i + 15; eight threads take four
+    // pieces of two neighbouring rows, whose swizzled places hit every bank once.  A half's bytes
+    // are loaded a whole block ahead, right after the last ones left their registers.
+    const int row0 = 2 * (tid >> 4) + ((tid >> 2) & 1), pc = 4 * ((tid >> 3) & 1) + (tid & 3);
+    constexpr int N = kC8tBlk / 16;  // pieces of a half
+    uint4 raw[2][N];
+    float rs[2][N];  // scales of the pieces' rows (0 past the last row)
+    auto load_raw = [&](int u, int h) {
+      if (u >= u1 || u >= lb) return;
+      const uint8_t *src = (h ? a.v8 : a.k8) + (bh * a.cap + static_cast<int64_t>(u) * kC8tBlk + row0) * D + 16 * pc;
+      const float *sc = (h ? a.vs : a.ks) + bh * (a.cap >> a.bl_shift);
+      const int left = n_loc - u * kC8tBlk;  // rows of the block
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        raw[h][i] = make_uint4(0, 0, 0, 0);
+        rs[h][i] = 0.0f;
+        if (left >= kC8tBlk || 16 * i + row0 < left) raw[h][i] = ld_stream16(src + 2048 * i);
+        if (16 * i < left) rs[h][i] = __ldg(sc + ((u * kC8tBlk + 16 * i) >> a.bl_shift));
+      }
+    };
+    load_raw(u0, 0);
+    load_raw(u0, 1);
+    const int nl = max(0, min(u1, lb) - u0);  // local blocks of this split
+    for (int j = 0; j < nl; ++j) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float mx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) mx = fmaxf(mx, rs[h][i]);
+        if (mx == 0.0f) mx = 1.0f;  // rows of zeros
+        const float inv = 1.0f / mx;  // a power of two
+        if (!wait_slot(j, h)) continue;
+        if (tid == 0) scales[2 * (j % (2 * kC8tSlots)) + h] = mx;
+        uint8_t *dst = slot(j, h);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float f = rs[h][i] * inv;
+          const __half2 f2 = __float2half2_rn(f), bias = __float2half2_rn(-1152.0f * f);
+          const uint4 x = raw[h][i];
+          const uint2 w0 = widen4_scaled<FMT>(x.x, f2, bias), w1 = widen4_scaled<FMT>(x.y, f2, bias);
+          const uint2 w2 = widen4_scaled<FMT>(x.z, f2, bias), w3 = widen4_scaled<FMT>(x.w, f2, bias);
+          *reinterpret_cast<uint4 *>(dst + ptc_swz(16 * i + row0, 2 * pc, kC8tBlk)) =
+              make_uint4(w0.x, w0.y, w1.x, w1.y);
+          *reinterpret_cast<uint4 *>(dst + ptc_swz(16 * i + row0, 2 * pc + 1, kC8tBlk)) =
+              make_uint4(w2.x, w2.y, w3.x, w3.y);
+        }
+        load_raw(u0 + j + 1, h);
+        landed(j, h);
+      }
+    }
+    // memory rows, bf16: pieces of 8 elements, 16 a row
+    const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
+    for (int j = nl; j < nblk; ++j) {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.content) + h * kv + g * D + 8 * (tid & 15);
+        const int x0 = (u0 + j - lb) * kC8tBlk + (tid >> 4);
+        constexpr int M = kC8tBlk / 8;
+        uint4 w[M];
+        float mx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          const int x = x0 + 8 * i;
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (x < n_mem) w[i] = *reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(table[x]) * 2 * kv);
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx = max3(mx, finite_abs(__uint_as_float(y[e] << 16)), finite_abs(__uint_as_float(y[e] & 0xffff0000u)));
+        }
+        mx = warp_max(mx);
+        asm volatile("bar.sync 1, %0;" ::"n"(kC8tConv) : "memory");  // `red` was read
+        if (lane == 0) red[warp - 10] = mx;
+        asm volatile("bar.sync 1, %0;" ::"n"(kC8tConv) : "memory");
+        mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        mx = mx > 0.0f ? floor_pow2(mx) : 1.0f;
+        if (!wait_slot(j, h)) continue;
+        if (tid == 0) scales[2 * (j % (2 * kC8tSlots)) + h] = mx;
+        const float inv = 1.0f / mx;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          uint32_t z[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            z[e] = pack_f16x2(__uint_as_float(y[e] << 16) * inv, __uint_as_float(y[e] & 0xffff0000u) * inv);
+          *reinterpret_cast<uint4 *>(slot(j, h) + ptc_swz(8 * i + (tid >> 4), tid & 15, kC8tBlk)) =
+              make_uint4(z[0], z[1], z[2], z[3]);
+        }
+        landed(j, h);
+      }
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks the loop, so that addresses and descriptors are warp-uniform values;
+    // lane 0 alone issues.
+    constexpr uint32_t idesc_s = umma_idesc_f16_f32<kC8tRows, kC8tBlk>();
+    constexpr uint32_t idesc_o = umma_idesc_f16_f32<kC8tRows, D>() | (1u << 16);  // B MN-major
+    const int x = warp - 8;
+    const int n = x == 0 || act1 ? nblk : 0;
+    // descriptors of the first slots; a step adds its offset in units of 16 bytes
+    const uint32_t base = smem_u32(sm);
+    const uint64_t q_desc = umma_desc_k_sw128(base + x * Sm::kQBytes), k_desc = umma_desc_k_sw128(base + Sm::kK);
+    const uint64_t v_desc = umma_desc_mn_sw128(base + Sm::kV, Sm::kKVBytes / 2);
+    const uint32_t o = tmem + kC8tTmemO + 128 * x;
+    bool ok = n > 0 && __all_sync(0xffffffffu, wait(kCbQ0 + x, 0));
+    // S of block j, once K has landed and its buffer is free: the P V two blocks back, which reads
+    // P there, has completed
+    auto scores = [&](int j) {
+      const int s = j % kC8tSlots, u = j & 1;
+      ok = ok && __all_sync(0xffffffffu, wait(kCbFullK0 + s, (j / kC8tSlots) & 1) &&
+                                             (j < 2 || wait(kCbO0 + 2 * x + u, ((j >> 1) - 1) & 1)));
+      if (!ok) return;
+      tc05_fence_after();
+      const uint64_t kd = k_desc + static_cast<uint32_t>(s * (Sm::kKVBytes >> 4));
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          umma_bf16(tmem + 128 * x + 64 * u, q_desc + ((i >> 2) * kC8tRows * 8 + (i & 3) * 2),
+                    kd + ((i >> 2) * kC8tBlk * 8 + (i & 3) * 2), idesc_s, i != 0);
+        umma_commit(bar(kCbS0 + 2 * x + u));
+        umma_commit(bar(kCbFreeK0 + s));
+      }
+      __syncwarp();
+    };
+    for (int j = 0; j < min(2, n); ++j) scores(j);
+    for (int j = 0; j < n; ++j) {
+      // P V once P is written (and O rescaled) and V has landed, then the S that P's buffer takes
+      const int s = j % kC8tSlots, u = j & 1;
+      ok = ok && __all_sync(0xffffffffu, wait(kCbFullV0 + s, (j / kC8tSlots) & 1) &&
+                                             wait(kCbP0 + 2 * x + u, (j >> 1) & 1));
+      if (!ok) break;
+      tc05_fence_after();
+      const uint64_t vd = v_desc + static_cast<uint32_t>(s * (Sm::kKVBytes >> 4));
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kC8tBlk / 16; ++i)
+          umma_f16_ts(o, tmem + 128 * x + 64 * u + 8 * i, vd + i * 128, idesc_o, (j | i) != 0);
+        umma_commit(bar(kCbO0 + 2 * x + u));
+        umma_commit(bar(kCbFreeV0 + s));
+      }
+      __syncwarp();
+      if (j + 2 < n) scores(j + 2);
+    }
+    // every MMA issued here completes before TMEM is freed
+    if (lane == 0) {
+      umma_commit(bar(kCbDrain + x));
+      mbar_wait(bar(kCbDrain + x), 0);
+    }
+    __syncwarp();
+  } else if (warp < 4 || act1) {
+    // ------------------------------------------------------------ softmax, tile x
+    const int x = warp >> 2, r = threadIdx.x & 127;
+    uint8_t *qs = sm + x * Sm::kQBytes;
+    const int col = c0 + x * kC8tRows + r, t = col_token(a, col);
+    const bool real = col < cols;
+    const int64_t orow = (static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + col - t * a.G;
+    float cf;  // score factor: scale_log2 * the power of two taken out of Q's row
+    {
+      uint4 w[16];
+      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.Q) + orow * D);
+      float mx = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mx = max3(mx, finite_abs(__uint_as_float(y[e] << 16)), finite_abs(__uint_as_float(y[e] & 0xffff0000u)));
+      }
+      const float p2 = mx > 0.0f ? floor_pow2(mx) : 1.0f, inv = 1.0f / p2;
+      cf = a.scale_log2 * p2;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t z[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          z[e] = pack_f16x2(__uint_as_float(y[e] << 16) * inv, __uint_as_float(y[e] & 0xffff0000u) * inv);
+        *reinterpret_cast<uint4 *>(qs + ptc_swz(r, i, kC8tRows)) = make_uint4(z[0], z[1], z[2], z[3]);
+      }
+    }
+    fence_proxy_async_smem();  // Q becomes visible to the tensor cores
+    mbar_arrive(bar(kCbQ0 + x));
+
+    const int vis = real ? column_rows(a, q, col) : 0;  // local rows the column sees
+    float m_run = -INFINITY, l_run = 0.0f, unit = kC8MinUnit;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tmem_s = tmem + 128 * x + lane_base, tmem_o = tmem + kC8tTmemO + 128 * x + lane_base;
+    bool okw = true;
+    for (int j = 0; j < nblk; ++j) {
+      const int u = u0 + j;
+      // V's barrier brings both scales
+      okw = __all_sync(0xffffffffu, wait(kCbFullV0 + j % kC8tSlots, (j / kC8tSlots) & 1) &&
+                                        wait(kCbS0 + 2 * x + (j & 1), (j >> 1) & 1));
+      if (!okw) break;
+      tc05_fence_after();
+      // (positive even where the product underflows, so that a hidden row stays at -inf)
+      float c = fmaxf(cf * scales[2 * (j % (2 * kC8tSlots))], 1.2e-38f);
+      const float v_scale = scales[2 * (j % (2 * kC8tSlots)) + 1];
+      const float unit_new = fmaxf(unit, v_scale);
+      // whole power of two: V's scale over the unit
+      const int lr = (__float_as_int(v_scale) >> 23) - (__float_as_int(unit_new) >> 23);
+      const int lim = u < lb ? vis - u * kC8tBlk : real ? n_mem - (u - lb) * kC8tBlk : 0;  // rows seen
+      const uint32_t at = tmem_s + kC8tBlk * (j & 1);
+      float s[kC8tBlk];
+      static_assert(kC8tBlk == 64, "one 64-column TMEM load per block");
+      tmem_ld64(at, s);
+      if (lim < kC8tBlk) {
+#pragma unroll
+        for (int i = 0; i < kC8tBlk; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < kC8tBlk; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
+      const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+      const float m_new = bm > m_run + kC8Slack ? bm + kC8Lead : m_run;
+      float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
+      const float mo = (m_new == -INFINITY ? 0.0f : m_new) - kC8Shift;
+      // the ratio of the scales in the exponent, unless it would take weights out of range
+      const bool fold = lr >= -24;
+      const float mf = fold ? mo - static_cast<float>(lr) : mo;
+      if (fabsf(m_new) > 262144.0f && m_new != -INFINITY) {
+        // far scores: the reference came from a rounded product, so the others are rounded alike
+#pragma unroll
+        for (int i = 0; i < kC8tBlk; ++i) s[i] = __fmul_rn(s[i], c);
+        c = 1.0f;
+      }
+      l_run *= alpha;
+      alpha *= unit / unit_new;
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+        // O's lane follows the reference and the unit, once the last P V has completed (TMEM
+        // accesses are warp-collective)
+        okw = __all_sync(0xffffffffu, wait(kCbO0 + 2 * x + ((j - 1) & 1), ((j - 1) >> 1) & 1));
+        if (!okw) break;
+        tc05_fence_after();
+#pragma unroll 1
+        for (int cc = 0; cc < D; cc += 32) {
+          uint32_t o[32];
+          tmem_ld32(tmem_o + cc, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st32(tmem_o + cc, o);
+        }
+      }
+      float2 ps[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int i = 0; i < kC8tBlk; i += 2) {
+        const float2 e = fma2(make_float2(s[i], s[i + 1]), make_float2(c, c), make_float2(-mf, -mf));
+        s[i] = ex2_approx(e.x);
+        s[i + 1] = ex2_approx(e.y);
+        ps[(i >> 1) & 1] = add2(ps[(i >> 1) & 1], make_float2(s[i], s[i + 1]));
+      }
+      if (!fold) {
+        const float ratio = v_scale / unit_new;
+#pragma unroll
+        for (int i = 0; i < kC8tBlk; ++i) s[i] *= ratio;
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = pack_f16x2(s[2 * i], s[2 * i + 1]);
+      tmem_st32(at, w);  // P over S
+      const float sum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
+      l_run += fold ? sum * __int_as_float((127 - lr) << 23) : sum;
+      m_run = m_new;
+      unit = unit_new;
+      tc05_fence_before();
+      mbar_arrive(bar(kCbP0 + 2 * x + (j & 1)));
+    }
+    if (okw && nblk > 0) okw = __all_sync(0xffffffffu, wait(kCbO0 + 2 * x + ((nblk - 1) & 1), ((nblk - 1) >> 1) & 1));
+    tc05_fence_after();
+    const bool have = okw && nblk > 0;
+    const bool one = a.n_split == 1;
+    // O in its own unit: over l for the result, times 2^-shift for a split's part
+    const float f = l_run == 0.0f ? 0.0f : one ? unit / l_run : unit * exp2f(-kC8Shift);
+    float *part = a.part_o + (orow * a.n_split + split) * D;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.O) + orow * D;
+#pragma unroll 1
+    for (int cc = 0; cc < D; cc += 16) {
+      float o[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+      if (have) tmem_ld16(tmem_o + cc, o);
+      if (!real) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = l_run == 0.0f ? 0.0f : o[i] * f;
+      if (one)
+        store16(out + cc, o);
+      else
+        store16(part + cc, o);
+    }
+    if (real) {
+      const float l = l_run * exp2f(-kC8Shift);
+      if (one) {
+        if (a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (m_run + log2f(l)) / kLog2e;
+      } else {
+        a.part_ml[(orow * a.n_split + split) * 2] = m_run;
+        a.part_ml[(orow * a.n_split + split) * 2 + 1] = l;
+      }
+    }
+  }
+  tc05_fence_before();
+  __syncthreads();
+  tc05_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, kC8tTmemCols);
+}
+
+}  // namespace msa

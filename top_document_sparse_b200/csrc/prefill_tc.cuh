@@ -89,12 +89,6 @@ struct PtcSmem {
   static int bytes(int table_cap) { return kFixed + table_cap * 4; }
 };
 
-// Byte offset of 16-byte chunk c (0 .. D/8) of row r of a [panel][rows][128 B]
-// tile of `rows` rows (128-byte swizzle: chunk index XOR row % 8).
-__device__ __forceinline__ uint32_t ptc_swz(int r, int c, int rows) {
-  return static_cast<uint32_t>((c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
 // grid n_pairs * B * H_kv (n_pairs = ceil(ceil(T * G / 128) / 2)), block
 // kPtcThreads, one CTA per SM: the tile pairs of one (query, kv head) are
 // adjacent in launch order, so they run at about the same time and read the

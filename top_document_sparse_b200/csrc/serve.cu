@@ -9,6 +9,7 @@
 
 #include "cache8.cuh"
 #include "cache8_attend.cuh"
+#include "cache8_prefill_tc.cuh"
 #include "rope.cuh"
 
 using namespace msa_host;
@@ -184,18 +185,53 @@ int attend8_nt(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 
 struct Attend8Plan {
   int n_split = 1, loc_split = 1, col_tiles = 1, table_cap = 0;
+  bool tc = false;  // tcgen05: col_tiles is then the number of tile pairs
   size_t part_o = 0, part_ml = 0, lse = 0, bytes = 0;
 };
+
+// Partial results of the splits, and the log-sums where weights are tracked without `lse`.
+void plan_attend8_scratch(Attend8Plan &p, const msa_memory *mem, const msa_cache8 *c, size_t rows) {
+  if (p.n_split > 1) {
+    p.part_ml = round256(rows * p.n_split * mem->D * 4);
+    p.bytes = p.part_ml + round256(rows * p.n_split * 2 * 4);
+  }
+  p.lse = p.bytes;
+  if (c->weights) p.bytes += round256(rows * 4);
+}
+
+int attend8_tc_cols() { const char *e = getenv("C8TC"); return e ? atoi(e) : 96; }
 
 Attend8Plan plan_attend8(const msa_memory *mem, const msa_cache8 *c, int T, int k, int H_q) {
   Attend8Plan p;
   const int64_t max_mem = static_cast<int64_t>(k) * mem->max_doc_chunks;
   p.table_cap = static_cast<int>(std::min<int64_t>(max_mem, msa::kMaxMemRows));
   const int64_t cols = static_cast<int64_t>(T) * (H_q / mem->H_kv);
+  const int64_t bh = static_cast<int64_t>(c->batch) * mem->H_kv;
+  const size_t rows = static_cast<size_t>(c->batch) * T * H_q;
+  p.tc = mem->dtype == MSA_BF16 && mem->D == 128 && cols >= attend8_tc_cols() &&
+         msa::C8tSmem::bytes(p.table_cap) <= max_dyn_smem();
+  if (p.tc) {
+    // context splits that finish first, counting a CTA's set-up and its part of the merge as
+    // eight blocks
+    p.col_tiles = static_cast<int>((cols + 2 * msa::kC8tRows - 1) / (2 * msa::kC8tRows));
+    const int64_t ctas = bh * p.col_tiles;
+    const int64_t blocks = (c->capacity + max_mem + msa::kC8tBlk - 1) / msa::kC8tBlk;
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= 16 && (s == 1 || s * 4 <= blocks); ++s) {
+      const int64_t waves = (ctas * s + num_sms() - 1) / num_sms();
+      const int64_t cost = waves * ((blocks + s - 1) / s + 8);
+      if (cost < best) {
+        best = cost;
+        p.n_split = p.loc_split = s;
+      }
+    }
+    plan_attend8_scratch(p, mem, c, rows);
+    return p;
+  }
   const int per = mem->dtype == MSA_BF16 ? 8 * attend8_nt(static_cast<int>(std::min<int64_t>(cols, 64)))
                                          : msa::kC8Cols32;
   p.col_tiles = static_cast<int>((cols + per - 1) / per);
-  const int64_t ctas = static_cast<int64_t>(c->batch) * mem->H_kv * p.col_tiles;
+  const int64_t ctas = bh * p.col_tiles;
   const int64_t want = 3LL * num_sms();
   // Splits of at most 2,048 local rows, so that ragged lengths spread over the SMs, and enough of
   // them for three CTAs an SM (64 queries of up to 8,192 rows: 133 us at 4,096 rows a split, 124
@@ -209,13 +245,7 @@ Attend8Plan plan_attend8(const msa_memory *mem, const msa_cache8 *c, int T, int 
     const int64_t own = std::min<int64_t>((max_mem + 63) / 64, std::max<int64_t>(1, want / ctas));
     p.n_split += static_cast<int>(std::min<int64_t>(own, 64));
   }
-  const size_t rows = static_cast<size_t>(c->batch) * T * H_q;
-  if (p.n_split > 1) {
-    p.part_ml = round256(rows * p.n_split * mem->D * 4);
-    p.bytes = p.part_ml + round256(rows * p.n_split * 2 * 4);
-  }
-  p.lse = p.bytes;  // used when the caller tracks weights without taking lse
-  if (c->weights) p.bytes += round256(rows * 4);
+  plan_attend8_scratch(p, mem, c, rows);
   return p;
 }
 
@@ -236,6 +266,19 @@ msa_status attend8_check(const msa_memory *mem, const msa_cache8 *c, int T, int 
   return MSA_OK;
 }
 
+template <int FMT>
+msa_status launch_prefill8(const msa::Attend8Args &a, const Attend8Plan &p, int B, cudaStream_t st) {
+  auto kern = msa::cache8_prefill_tc_kernel<FMT>;
+  const int smem = msa::C8tSmem::bytes(p.table_cap);
+  MSA_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const int64_t ctas = static_cast<int64_t>(B) * a.H_kv * p.col_tiles;
+  if (ctas > 0x7FFFFFFF) return fail(MSA_ERR_UNSUPPORTED, "too many query tokens");
+  MSA_CUDA(launch_pdl(kern, dim3(static_cast<unsigned>(ctas), p.n_split), dim3(msa::kC8tThreads), smem,
+                      st, a, p.col_tiles));
+  MSA_LAUNCHED("cache8_prefill_tc_kernel");
+  return MSA_OK;
+}
+
 template <typename T, int D, int FMT, int NT>
 msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B, cudaStream_t st) {
   constexpr bool kBf16 = sizeof(T) == 2;
@@ -249,9 +292,14 @@ msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B
     kern = msa::cache8_attend_f32_kernel<D, FMT>;
     smem = msa::Attend8Smem32<D>::bytes(p.table_cap);
   }
-  MSA_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  MSA_CUDA(launch_pdl(kern, grid, block, smem, st, a));
-  MSA_LAUNCHED("cache8_attend_kernel");
+  if (kBf16 && D == 128 && p.tc) {
+    const msa_status s = launch_prefill8<FMT>(a, p, B, st);
+    if (s != MSA_OK) return s;
+  } else {
+    MSA_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    MSA_CUDA(launch_pdl(kern, grid, block, smem, st, a));
+    MSA_LAUNCHED("cache8_attend_kernel");
+  }
   if (p.n_split > 1) {
     MSA_CUDA(launch_pdl(msa::cache8_combine_kernel<T>,
                         dim3(static_cast<unsigned>(B * a.T * a.H_kv * a.G)), dim3(D), 0, st, a, D));

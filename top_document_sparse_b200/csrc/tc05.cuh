@@ -38,6 +38,12 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t 
   return d;
 }
 
+// Byte offset of 16-byte chunk c (0 .. D/8) of row r of a [panel][rows][128 B]
+// tile of `rows` rows (128-byte swizzle: chunk index XOR row % 8).
+__device__ __forceinline__ uint32_t ptc_swz(int r, int c, int rows) {
+  return static_cast<uint32_t>((c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
 // Instruction descriptor, kind::f16: bf16 A and B (both K-major), fp32 D,
 // M x N tile.
 template <int M, int N>
