@@ -77,25 +77,51 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= 3.402823466e38f ? a : 0.0f;
 }
 
-// 16 consecutive elements of T as floats (64 or 32 bytes, 16-byte aligned)
+// 16 consecutive elements as they lie in memory (64 or 32 bytes, 16-byte aligned), and as floats.
 template <typename T>
-__device__ __forceinline__ void load16(const T *p, float v[16]) {
-  if constexpr (sizeof(T) == 4) {
+struct Raw16 {
+  static constexpr int N = sizeof(T);  // 16-byte pieces (sizeof(T) * 16 / 16)
+  uint4 x[N];
+  __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load4(p + 4 * i, v + 4 * i);
-  } else {
+    for (int i = 0; i < N; ++i) x[i] = *(reinterpret_cast<const uint4 *>(p) + i);
+  }
+  __device__ __forceinline__ void get(float v[16]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(p + 8 * i);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (int i = 0; i < N; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-        v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        if constexpr (sizeof(T) == 4) {
+          v[4 * i + j] = __uint_as_float(w[j]);
+        } else {
+          v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+          v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
       }
     }
   }
-}
+  // The largest magnitude's bits as fp32: magnitudes order like integers, infinities and NaN above
+  // all finite ones.
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4)
+          m = max(m, w[j] & 0x7fffffffu);
+        else
+          asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[j] & 0x7fff7fffu));
+      }
+    }
+    if constexpr (sizeof(T) == 2) m = max(m & 0xffff0000u, m << 16);
+    return m;
+  }
+};
+constexpr uint32_t kInfBits = 0x7f800000u;
+
 template <typename T>
 __device__ __forceinline__ void store16(T *p, const float v[16]) {
   if constexpr (sizeof(T) == 4) {
@@ -113,14 +139,27 @@ __device__ __forceinline__ void store16(T *p, const float v[16]) {
     }
   }
 }
+// 16 values / scale as bytes.  `finite`: none is infinite or NaN.
 template <int FMT>
-__device__ __forceinline__ uint4 pack16(const float v[16], float inv) {
+__device__ __forceinline__ uint4 pack16(const float v[16], float inv, bool finite) {
+  if (FMT == MSA_CACHE_INT8 && finite) {
+    // adding 1.5 * 2^23 rounds to a whole number, ties to even, in the low bits of the sum
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(fmaf(v[4 * i + j], inv, 12582912.0f));
+      w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float y[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = to_grid<FMT>(v[4 * i + j], inv);
+    for (int j = 0; j < 4; ++j) y[j] = finite ? v[4 * i + j] * inv : to_grid<FMT>(v[4 * i + j], inv);
     w[i] = Fmt8<FMT>::pack4(y);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -176,7 +215,7 @@ template <typename T, int D, int FMT, int NT>
 __global__ void __launch_bounds__(256)
 cache8_append_kernel(AppendArgs a, int set_len) {
   constexpr int CPR = D / 16;
-  __shared__ float red[8];
+  __shared__ uint32_t red[8];
   griddep_wait();
   griddep_launch();
   const int h = blockIdx.x >> 1, which = blockIdx.x & 1, b = blockIdx.z;
@@ -195,37 +234,59 @@ cache8_append_kernel(AppendArgs a, int set_len) {
   const int64_t bh = static_cast<int64_t>(b) * a.H_kv + h;
   uint8_t *dst = (which ? a.v8 : a.k8) + (bh * a.cap + x0) * D;
   float *scale = (which ? a.vs : a.ks) + bh * (a.cap / a.bl) + blk;
-  float v[NT][16];
-  float amax = 0.0f;
+  Raw16<T> v[NT];
+  uint32_t top = 0;
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
     const int task = threadIdx.x + 256 * u, row = x0 + task / CPR;
-    if (row >= lo && row < hi) {
-      load16(src + (row - r.start) * ts + (task % CPR) * 16, v[u]);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(v[u][i]));
-    }
+    if (row >= lo && row < hi) v[u].load(src + (row - r.start) * ts + (task % CPR) * 16);
   }
-  amax = warp_max(amax);
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) amax = fmaxf(amax, red[w]);
   const float s_old = lo > x0 ? *scale : 0.0f;
-  const float s = fmaxf(block_scale<FMT>(amax), s_old);
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const int row = x0 + (threadIdx.x + 256 * u) / CPR;
+    if (row >= lo && row < hi) top = max(top, v[u].amax_bits());
+  }
+  auto cta_max = [&](uint32_t m) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = m;
+    __syncthreads();  // (every thread has read the old scale, too)
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = max(m, red[w]);
+    return m;
+  };
+  top = cta_max(top);
+  const bool finite = top < kInfBits;
+  if (!finite) {  // the largest finite magnitude
+    top = 0;
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int row = x0 + (threadIdx.x + 256 * u) / CPR;
+      if (row >= lo && row < hi) {
+        float x[16];
+        v[u].get(x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(finite_abs(x[i])));
+      }
+    }
+    __syncthreads();
+    top = cta_max(top);
+  }
+  const float s = fmaxf(block_scale<FMT>(__uint_as_float(top)), s_old);
   const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-  __syncthreads();  // every thread has read the old scale
   if (threadIdx.x == 0 && (s != s_old || lo == x0)) *scale = s;
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
     const int task = threadIdx.x + 256 * u, row = x0 + task / CPR;
     uint4 *p = reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(task) * 16);
     if (row >= lo && row < hi) {
-      *p = pack16<FMT>(v[u], inv);
+      float x[16];
+      v[u].get(x);
+      *p = pack16<FMT>(x, inv, finite);
     } else if (row < lo && s > s_old) {  // earlier rows of a block whose scale grew
       float old[16];
       unpack16<FMT>(*p, s_old, old);
-      *p = pack16<FMT>(old, inv);
+      *p = pack16<FMT>(old, inv, true);
     }
   }
   if (a.weights && which == 0)
@@ -323,12 +384,14 @@ __device__ __forceinline__ int cta_prefix(bool flag, int *warp_sums, int *total)
 // A block's weight is summed in 64 bits and compared in 32, so the choice does not hang on the
 // order of the sum.  The keep - recent heaviest of the older blocks: a radix select over the keys
 // (four passes of 8 bits) finds the smallest kept key, then one pass in block order keeps all
-// larger keys and the first of the equal ones.
+// larger keys and the first of the equal ones.  The keys lie in shared memory where they fit
+// (smem_keys), else in the workspace.  Bound by latency: a dozen barriers of one CTA a head.
 __global__ void __launch_bounds__(kSelThreads)
 cache8_select_kernel(const float *__restrict__ weights, const int32_t *__restrict__ cache_len,
-                     int H_kv, int cap, int bl, int budget, int recent,
+                     int H_kv, int cap, int bl, int budget, int recent, int smem_keys,
                      uint32_t *__restrict__ keys, int32_t *__restrict__ src_block,
                      int32_t *__restrict__ lens) {
+  extern __shared__ uint32_t key_sm[];
   __shared__ int hist[256];
   __shared__ int warp_sums[kSelThreads / 32];
   __shared__ int digit, above;
@@ -342,7 +405,7 @@ cache8_select_kernel(const float *__restrict__ weights, const int32_t *__restric
     lens[2 * b + 1] = p.new_len;
   }
   int32_t *src = src_block + bh * (nb + 1);
-  uint32_t *key = keys + bh * nb;
+  uint32_t *key = smem_keys ? key_sm : keys + bh * nb;
   const int old = p.full - p.recent;     // blocks that compete
   const int want = p.keep - p.recent;    // of which these stay
   if (threadIdx.x == 0 && p.tail > 0) src[p.keep] = p.full;
@@ -351,41 +414,60 @@ cache8_select_kernel(const float *__restrict__ weights, const int32_t *__restric
     for (int j = threadIdx.x; j < old; j += kSelThreads) src[j] = j;
     return;
   }
-  const float *w = weights + bh * cap;
-  for (int j = threadIdx.x; j < old; j += kSelThreads) {
-    double s = 0.0;
-    const float4 *row = reinterpret_cast<const float4 *>(w + static_cast<int64_t>(j) * bl);
-    for (int i = 0; i < bl / 4; ++i) {
-      const float4 x = row[i];
-      s += static_cast<double>(x.x);
-      s += static_cast<double>(x.y);
-      s += static_cast<double>(x.z);
-      s += static_cast<double>(x.w);
-    }
-    key[j] = weight_key(static_cast<float>(s));
-  }
   if (want == 0) return;
+  const int lane = threadIdx.x % 32;
+  {
+    // bl / 4 neighbouring lanes sum a block
+    const int per = bl / 4, blocks = kSelThreads / per;
+    const float4 *w = reinterpret_cast<const float4 *>(weights + bh * cap);
+    for (int j0 = 0; j0 < old; j0 += blocks) {  // (whole warps stay together)
+      const int j = j0 + threadIdx.x / per;
+      double s = 0.0;
+      if (j < old) {
+        const float4 x = w[static_cast<int64_t>(j) * per + threadIdx.x % per];
+        s = (static_cast<double>(x.x) + x.y) + (static_cast<double>(x.z) + x.w);
+      }
+      for (int o = per / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (j < old && threadIdx.x % per == 0) key[j] = weight_key(static_cast<float>(s));
+    }
+  }
   uint32_t prefix = 0, mask = 0;
   int left = want;  // the left-th largest key among those that match the prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
+    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+    __syncthreads();  // (and the keys are written)
     for (int j = threadIdx.x; j < old; j += kSelThreads)
       if ((key[j] & mask) == prefix) atomicAdd(&hist[(key[j] >> shift) & 255], 1);
     __syncthreads();
-    if (threadIdx.x == 0) {
-      int n = 0, d = 255;
-      for (; d > 0; --d) {
-        if (n + hist[d] >= left) break;
-        n += hist[d];
+    if (threadIdx.x < 32) {
+      // eight digits a lane, from the largest down; lanes before this one hold larger digits
+      int n[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[i] = hist[255 - 8 * lane - i];
+        sum += n[i];
       }
-      digit = d;
-      above = n;
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      before -= sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (before < left && before + n[i] >= left) {
+          digit = 255 - 8 * lane - i;
+          above = before;
+        }
+        before += n[i];
+      }
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(digit) << shift;
     mask |= 255u << shift;
     left -= above;
+    __syncthreads();
   }
   // `prefix` is the smallest kept key, `left` of the blocks that have it stay (the first ones)
   int kept = 0, equal = 0;
@@ -431,7 +513,6 @@ cache8_move_kernel(EvictMove m, const int32_t *__restrict__ src_block,
   const int pieces = m.bl * m.D / 16, wp = m.bl / 4;
   const int s = blockIdx.x * 128 + threadIdx.x;
   if (s == 0 && blockIdx.y % m.H_kv == 0 && blockIdx.z == 0) m.out_len[b] = new_len;
-  // weights of rows no longer held (the out-of-place cache's own, up to its capacity)
   const int live = (new_len + m.bl - 1) / m.bl;  // blocks written
   const int per = (live + gridDim.z - 1) / gridDim.z;
   const int j0 = blockIdx.z * per, j1 = min(live, j0 + per);
@@ -486,6 +567,18 @@ cache8_move_kernel(EvictMove m, const int32_t *__restrict__ src_block,
           }
         }
     }
+    if (is_w && blockIdx.z == gridDim.z - 1) {
+      // the weights of rows that the query no longer holds (this thread has loaded every weight
+      // that may lie there)
+      const int end = min(lens[2 * b], m.out_cap);
+      float *o = m.ow + bh * m.out_cap;
+      for (int j = tail ? live - 1 : live; j * m.bl < end; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = j * m.bl + row + i;
+          if (x >= new_len && x < end) o[x] = 0.0f;
+        }
+    }
     return;
   }
   const bool v = s == 2 * pieces + wp + 1;
@@ -500,17 +593,6 @@ cache8_move_kernel(EvictMove m, const int32_t *__restrict__ src_block,
     for (int u = 0; u < kMoveWave; ++u)
       if (j + u < j1) out[j + u] = x[u];
   }
-}
-
-// grid (B * H_kv): weights of the rows new_len .. min(len, capacity of out) become 0.
-__global__ void cache8_clear_weights_kernel(float *__restrict__ w, int H_kv, int cap,
-                                            const int32_t *__restrict__ lens) {
-  griddep_wait();
-  griddep_launch();
-  const int b = blockIdx.x / H_kv;
-  const int end = min(lens[2 * b], cap);
-  float *row = w + static_cast<int64_t>(blockIdx.x) * cap;
-  for (int x = lens[2 * b + 1] + threadIdx.x; x < end; x += blockDim.x) row[x] = 0.0f;
 }
 
 }  // namespace msa

@@ -806,9 +806,14 @@ cache8_attend_f32_kernel(Attend8Args a) {
 }
 
 // ---------------------------------------------------------------- combine
-// grid (B * T * H_q), block D: merge the context splits.
+// grid (B * T * H_q), block D: merge the context splits (at most kC8MaxSplit).  One warp turns the
+// splits' references and sums into factors, then a thread an element adds the parts.
+constexpr int kC8MaxSplit = 128;
 template <typename T>
-__global__ void cache8_combine_kernel(Attend8Args a, int D) {
+__global__ void __launch_bounds__(128)
+cache8_combine_kernel(Attend8Args a, int D) {
+  __shared__ float f[kC8MaxSplit];
+  __shared__ float total;
   griddep_wait();
   griddep_launch();
   const int64_t row = blockIdx.x;
@@ -816,56 +821,90 @@ __global__ void cache8_combine_kernel(Attend8Args a, int D) {
   const int b = static_cast<int>(row / H_q / a.T), t = static_cast<int>(row / H_q % a.T);
   const Attend8Query q = attend8_query(a, b, false);
   if (t >= q.n) return;
-  const float *ml = a.part_ml + row * a.n_split * 2;
-  float M = -INFINITY;
-  for (int s = 0; s < a.n_split; ++s) M = fmaxf(M, ml[2 * s]);
-  const float base = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f, o = 0.0f;
-  for (int s = 0; s < a.n_split; ++s) {
-    const float f = exp2f(ml[2 * s] - base);
-    L += ml[2 * s + 1] * f;
-    o += a.part_o[(row * a.n_split + s) * D + threadIdx.x] * f;
+  const int n = a.n_split;
+  if (threadIdx.x < 32) {
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + row * n;
+    float2 x[kC8MaxSplit / 32];
+    float M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kC8MaxSplit / 32; ++i) {
+      const int s = threadIdx.x + 32 * i;
+      x[i] = s < n ? ml[s] : make_float2(-INFINITY, 0.0f);
+      M = fmaxf(M, x[i].x);
+    }
+    M = warp_max(M);
+    const float base = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+    for (int i = 0; i < kC8MaxSplit / 32; ++i) {
+      const float e = exp2f(x[i].x - base);
+      f[threadIdx.x + 32 * i] = e;
+      L += x[i].y * e;
+    }
+    L = warp_sum(L);
+    if (threadIdx.x == 0) {
+      total = L;
+      if (a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
+    }
   }
-  static_cast<T *>(a.O)[row * D + threadIdx.x] = Elem<T>::from_f(L == 0.0f ? 0.0f : o / L);
-  if (threadIdx.x == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
+  __syncthreads();
+  const float *part = a.part_o + row * n * D + threadIdx.x;
+  float o = 0.0f;
+#pragma unroll 8
+  for (int s = 0; s < n; ++s) o = fmaf(part[static_cast<int64_t>(s) * D], f[s], o);
+  static_cast<T *>(a.O)[row * D + threadIdx.x] = Elem<T>::from_f(total == 0.0f ? 0.0f : o / total);
 }
 
 // ---------------------------------------------------------------- weights
 // The weight each cached row received: with the softmax's log-sum known, a second pass over K
-// alone recomputes the scores, p = 2^(s - lse), and sums them over the columns.  A warp keeps
-// 16 rows as MMA operands and walks over all columns, staged 8 NT at a time in shared memory.
-// grid (ceil(cap / 64), B * H_kv), block 32 * kC8Warps.  fp32 memories: see below.
+// alone recomputes the scores, p = 2^(s - lse), and sums them over the columns.  A CTA copies
+// kC8wRows rows to shared memory once and walks over all columns, 8 NT at a time with Q's fragments
+// in registers; a warp's tiles keep their sums in registers.  Few columns: bound by K's bytes.
+// grid (ceil(cap / kC8wRows), B * H_kv), block 32 * kC8Warps.  fp32 memories: see below.
+constexpr int kC8wTiles = 4;                              // 16-row tiles a warp
+constexpr int kC8wRows = 16 * kC8wTiles * kC8Warps;
+template <int D, int NT>
+struct Weight8Smem {
+  static constexpr int kK = Attend8Smem<D, NT>::kMerge;   // behind Q and its scales
+  static constexpr int kLse = kK + kC8wRows * D;
+  static constexpr int kBytes = kLse + 8 * NT * 4;
+};
 template <int D, int NT, int FMT>
 __global__ void __launch_bounds__(32 * kC8Warps)
 cache8_weight_kernel(Attend8Args a) {
   using Sm = Attend8Smem<D, NT>;
+  using Wm = Weight8Smem<D, NT>;
   constexpr int KS = D / 16;
-  __shared__ __align__(16) uint8_t sm[Sm::kMerge];
-  __shared__ float lse2[Sm::kCols];
+  extern __shared__ __align__(16) uint8_t sm[];
+  float *lse2 = reinterpret_cast<float *>(sm + Wm::kLse);
   griddep_wait();
   griddep_launch();
   const int b = blockIdx.y / a.H_kv, g = blockIdx.y % a.H_kv;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, lg = lane >> 2, lt = lane & 3;
   const Attend8Query q = attend8_query(a, b, false);
-  if (static_cast<int>(blockIdx.x) * 64 >= q.len) return;
-  const int x0 = blockIdx.x * 64 + warp * 16;
-  const bool work = x0 < q.len;
+  const int r0 = blockIdx.x * kC8wRows;
+  if (r0 >= q.len) return;
   const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
-  uint32_t ka[KS][4];
-  float k_scale = 0.0f;
-  if (work) {
-    KTile<D> kt;
-    kt.from_global(a.k8 + (bh * a.cap + x0) * D, lane);
-    k_scale = a.ks[(bh * a.cap + x0) >> a.bl_shift];
+  // tile i of this warp: rows r0 + 16 (kC8Warps i + warp) ..
+  auto tile_row = [&](int i) { return r0 + 16 * (kC8Warps * i + warp); };
+  const uint32_t ring = smem_u32(sm + Wm::kK) + warp * kC8wTiles * Tile8<D>::kBytes;
+  float k_scale[kC8wTiles], sum[kC8wTiles][2];
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      widen4<FMT>(kt.w[0][i], ka[i][0], ka[i][2]);
-      widen4<FMT>(kt.w[1][i], ka[i][1], ka[i][3]);
+  for (int i = 0; i < kC8wTiles; ++i) {
+    const int x0 = tile_row(i);
+    k_scale[i] = sum[i][0] = sum[i][1] = 0.0f;
+    if (x0 < q.len) {
+      const uint8_t *src = a.k8 + (bh * a.cap + x0) * D;
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        const int p = lane + 32 * u;
+        cp_async_16(ring + i * Tile8<D>::kBytes + Tile8<D>::k_off(p / (D / 16), p % (D / 16)), src + 16 * p, true);
+      }
+      k_scale[i] = a.ks[(bh * a.cap + x0) >> a.bl_shift];
     }
   }
+  cp_async_commit();
   const __half *qh = reinterpret_cast<const __half *>(sm + Sm::kQ);
   const float *cs = reinterpret_cast<const float *>(sm + Sm::kColScale);
-  float sum[2] = {0.0f, 0.0f};
   for (int c0 = 0; c0 < q.n * a.G; c0 += Sm::kCols) {
     if (c0) __syncthreads();
     load_q_columns<D, NT>(a, b, g, c0, q.n, sm);
@@ -878,34 +917,72 @@ cache8_weight_kernel(Attend8Args a) {
       }
       lse2[c] = v;
     }
+    cp_async_wait<0>();
     __syncthreads();
-    if (!work) continue;
+    const int all_see = column_rows(a, q, c0);  // rows that every column of this round sees
+    uint32_t qf[NT][KS][2];
+    float cf[NT][2], ls[NT][2];
+    int rows[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         const uint2 x = *reinterpret_cast<const uint2 *>(qh + (8 * nt + lg) * Sm::kQPitch + k_elem(i, lt));
-        mma_f16_16816(s, ka[i][0], ka[i][1], ka[i][2], ka[i][3], x.x, x.y);
+        qf[nt][i][0] = x.x;
+        qf[nt][i][1] = x.y;
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = 8 * nt + 2 * lt + (e & 1), row = x0 + lg + 8 * (e >> 1);
-        const float p = exp2f(s[e] * (cs[c] * k_scale) - lse2[c]);
-        sum[e >> 1] += row < column_rows(a, q, c0 + c) ? p : 0.0f;
+      for (int h = 0; h < 2; ++h) {
+        const int c = 8 * nt + 2 * lt + h;
+        cf[nt][h] = cs[c];
+        ls[nt][h] = lse2[c];
+        rows[nt][h] = column_rows(a, q, c0 + c);
       }
     }
-  }
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-    const int row = x0 + lg + 8 * r;
-    if (work && lt == 0 && row < q.len) {
-      float *w = a.weights + bh * a.cap + row;
-      *w = a.decay == 0.0f ? sum[r] : a.decay * *w + sum[r];
+    for (int i = 0; i < kC8wTiles; ++i) {
+      const int x0 = tile_row(i);
+      if (x0 >= q.len) break;
+      KTile<D> kt;
+      kt.from_shared(ring + i * Tile8<D>::kBytes, lane);
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a0, a1, a2, a3;
+        widen4<FMT>(kt.w[0][k], a0, a2);
+        widen4<FMT>(kt.w[1][k], a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
+      }
+      const bool masked = x0 + 16 > all_see;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float p = ex2_approx(s[nt][e] * (cf[nt][e & 1] * k_scale[i]) - ls[nt][e & 1]);
+          if (masked && x0 + lg + 8 * (e >> 1) >= rows[nt][e & 1]) p = 0.0f;
+          sum[i][e >> 1] += p;
+        }
     }
   }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int i = 0; i < kC8wTiles; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float x = sum[i][r];
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      const int row = tile_row(i) + lg + 8 * r;
+      if (lt == 0 && row < q.len) {
+        float *w = a.weights + bh * a.cap + row;
+        *w = a.decay == 0.0f ? x : a.decay * *w + x;
+      }
+    }
 }
 
 // The same on CUDA cores: a lane on each of 32 rows, Q broadcast from shared memory.

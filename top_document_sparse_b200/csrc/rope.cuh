@@ -13,7 +13,7 @@
 
 namespace msa {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 512;  // most threads of a block
 constexpr int kRopeMaxDim = 512;
 
 struct RopeSide {  // one of Q and K: heads of `D` elements, strides in elements
@@ -80,7 +80,7 @@ __device__ __forceinline__ void rope_task(const T *in, T *out, int task, int rot
   }
 }
 
-// grid ceil(tokens / tok_cta), block kRopeThreads, shared tok_cta * r / 2 float2.
+// grid ceil(tokens / tok_cta), block <= kRopeThreads, shared tok_cta * r / 2 float2.
 // per_head = rot_tasks + the tasks of the copied rest (0 where the rest stays
 // in place).
 template <typename T, int V, bool INTER>
@@ -94,7 +94,7 @@ rope_kernel(const uint64_t *__restrict__ freq, int r, int D, float magnitude, in
   const int half = r >> 1;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok_cta;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tok_cta), tokens - t0));
-  for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+  for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
     const int t = i / half, p = i - t * half;
     const uint64_t turn = static_cast<uint64_t>(positions[t0 + t]) * freq[p];
     float s, c;
@@ -104,7 +104,7 @@ rope_kernel(const uint64_t *__restrict__ freq, int r, int D, float magnitude, in
   }
   __syncthreads();
   const int per_token = (q.heads + k.heads) * per_head;
-  for (int i = threadIdx.x; i < nt * per_token; i += kRopeThreads) {
+  for (int i = threadIdx.x; i < nt * per_token; i += blockDim.x) {
     const int t = i / per_token, j = i - t * per_token;
     const int h = j / per_head, task = j - h * per_head;
     const bool is_q = h < q.heads;

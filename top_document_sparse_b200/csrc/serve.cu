@@ -76,12 +76,16 @@ msa_status launch_rope(const msa_rope *rope, int64_t tokens, const int64_t *pos,
   const int rot = (V == 1 || !INTER) ? half / V : rope->r / V;
   const int rest = copy_rest ? (rope->D - rope->r) / V : 0;
   // tokens a CTA: enough tasks for every thread
+  // one task a thread where a token's tasks fit a block, so that no round runs half empty (40 heads
+  // of 128: 320 threads, 70 -> XX us against blocks of 256 for 16,384 tokens)
   const int per_token = (q.heads + k.heads) * (rot + rest);
-  const int tok = std::max(1, std::min(16, msa::kRopeThreads / std::max(per_token, 1)));
+  const int tok = std::max(1, std::min(16, 256 / std::max(per_token, 1)));
+  const int rounds = (tok * per_token + msa::kRopeThreads - 1) / msa::kRopeThreads;
+  const int threads = round32((tok * per_token + rounds - 1) / rounds);
   const int64_t grid = (tokens + tok - 1) / tok;
   if (grid > 0x7FFFFFFF) return fail(MSA_ERR_UNSUPPORTED, "too many tokens");
   MSA_CUDA(launch_pdl(msa::rope_kernel<T, V, INTER>, dim3(static_cast<unsigned>(grid)),
-                      dim3(msa::kRopeThreads), static_cast<size_t>(tok) * half * sizeof(float2), st,
+                      dim3(threads), static_cast<size_t>(tok) * half * sizeof(float2), st,
                       static_cast<const uint64_t *>(rope->d_freq), rope->r, rope->D,
                       rope->magnitude, inverse, pos, tokens, tok, q, k, rot, rot + rest));
   MSA_LAUNCHED("rope_kernel");
@@ -199,7 +203,11 @@ void plan_attend8_scratch(Attend8Plan &p, const msa_memory *mem, const msa_cache
   if (c->weights) p.bytes += round256(rows * 4);
 }
 
-int attend8_tc_cols() { const char *e = getenv("C8TC"); return e ? atoi(e) : 96; }
+// Columns (tokens * heads of a group) from which the tcgen05 kernel takes over.  It widens every
+// context row once for 256 columns, the other one once for 32: at 32 columns it takes 26 against
+// 44 us for one query of 8,192 rows but 397 against 210 for 32 of them (bound by the widening); at
+// 48 columns 27 against 42 and 397 against 385; at 128 columns 32 against 54 and 396 against 801.
+constexpr int64_t kTcCols = 48;
 
 Attend8Plan plan_attend8(const msa_memory *mem, const msa_cache8 *c, int T, int k, int H_q) {
   Attend8Plan p;
@@ -208,7 +216,7 @@ Attend8Plan plan_attend8(const msa_memory *mem, const msa_cache8 *c, int T, int 
   const int64_t cols = static_cast<int64_t>(T) * (H_q / mem->H_kv);
   const int64_t bh = static_cast<int64_t>(c->batch) * mem->H_kv;
   const size_t rows = static_cast<size_t>(c->batch) * T * H_q;
-  p.tc = mem->dtype == MSA_BF16 && mem->D == 128 && cols >= attend8_tc_cols() &&
+  p.tc = mem->dtype == MSA_BF16 && mem->D == 128 && cols >= kTcCols &&
          msa::C8tSmem::bytes(p.table_cap) <= max_dyn_smem();
   if (p.tc) {
     // context splits that finish first, counting a CTA's set-up and its part of the merge as
@@ -243,7 +251,7 @@ Attend8Plan plan_attend8(const msa_memory *mem, const msa_cache8 *c, int T, int 
   p.n_split = p.loc_split = static_cast<int>(loc);
   if (mem->dtype == MSA_BF16 && max_mem > 0 && (loc > 1 || ctas < want)) {
     const int64_t own = std::min<int64_t>((max_mem + 63) / 64, std::max<int64_t>(1, want / ctas));
-    p.n_split += static_cast<int>(std::min<int64_t>(own, 64));
+    p.n_split += static_cast<int>(std::min<int64_t>(own, msa::kC8MaxSplit - 64));
   }
   plan_attend8_scratch(p, mem, c, rows);
   return p;
@@ -306,10 +314,13 @@ msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B
     MSA_LAUNCHED("cache8_combine_kernel");
   }
   if (a.weights) {
-    if constexpr (kBf16)
-      MSA_CUDA(launch_pdl(msa::cache8_weight_kernel<D, NT, FMT>,
-                          dim3((a.cap + 63) / 64, B * a.H_kv), block, 0, st, a));
-    else
+    if constexpr (kBf16) {
+      auto wk = msa::cache8_weight_kernel<D, NT, FMT>;
+      const int ws = msa::Weight8Smem<D, NT>::kBytes;
+      MSA_CUDA(cudaFuncSetAttribute(wk, cudaFuncAttributeMaxDynamicSharedMemorySize, ws));
+      MSA_CUDA(launch_pdl(wk, dim3((a.cap + msa::kC8wRows - 1) / msa::kC8wRows, B * a.H_kv), block, ws,
+                          st, a));
+    } else
       MSA_CUDA(launch_pdl(msa::cache8_weight_f32_kernel<D, FMT>,
                           dim3((a.cap + 127) / 128, B * a.H_kv), block, 0, st, a));
     MSA_LAUNCHED("cache8_weight_kernel");
@@ -581,10 +592,13 @@ msa_status msa_cache8_evict(const msa_memory *mem, const msa_cache8 *cache, cons
   const cudaStream_t st = to_stream(stream);
   const unsigned bh = static_cast<unsigned>(cache->batch * mem->H_kv);
   const int bl = cache->block_len;
-  MSA_CUDA(launch_pdl(msa::cache8_select_kernel, dim3(bh), dim3(msa::kSelThreads), 0, st,
+  // the keys of up to 10,240 blocks fit in the 48 KB that need no opt-in beside the histogram
+  const int nb = cache->capacity / bl, smem_keys = nb <= 10240 ? 1 : 0;
+  MSA_CUDA(launch_pdl(msa::cache8_select_kernel, dim3(bh), dim3(msa::kSelThreads),
+                      smem_keys ? static_cast<size_t>(nb) * 4 : 0, st,
                       static_cast<const float *>(cache->weights),
                       static_cast<const int32_t *>(cache->cache_len), mem->H_kv, cache->capacity, bl,
-                      budget, recent, keys, src, lens));
+                      budget, recent, smem_keys, keys, src, lens));
   MSA_LAUNCHED("cache8_select_kernel");
   msa::EvictMove m;
   m.k8 = static_cast<const uint8_t *>(cache->k);
@@ -610,9 +624,6 @@ msa_status msa_cache8_evict(const msa_memory *mem, const msa_cache8 *cache, cons
                       st, m, static_cast<const int32_t *>(src), static_cast<const int32_t *>(lens),
                       in_place ? 1 : 0));
   MSA_LAUNCHED("cache8_move_kernel");
-  MSA_CUDA(launch_pdl(msa::cache8_clear_weights_kernel, dim3(bh), dim3(256), 0, st, out->weights,
-                      mem->H_kv, out->capacity, static_cast<const int32_t *>(lens)));
-  MSA_LAUNCHED("cache8_clear_weights_kernel");
   return MSA_OK;
 }
 
