@@ -31,7 +31,8 @@ template <> struct Fmt8<MSA_CACHE_INT8> {
   }
   static __device__ __forceinline__ void unpack4(uint32_t w, float v[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * i)));
+    for (int i = 0; i < 4; ++i)  // the bits of 2^23 + (q + 128), less 2^23 + 128
+      v[i] = __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7650 + i)) - 8388736.0f;
   }
 };
 
@@ -207,18 +208,23 @@ struct AppendArgs {
   float *weights;
 };
 
-// grid (2 * H_kv, blocks a query can touch, B), block 256: one CTA quantises the new rows of one
-// block of one head of K or V.  A task is 16 elements of a row, NT tasks a thread, so the block's
-// new rows stay in registers between the maximum and the rounding.  set_len: write the new
-// cache_len here (start given: no CTA reads cache_len).
-template <typename T, int D, int FMT, int NT>
-__global__ void __launch_bounds__(256)
+// grid (ceil(2 * H_kv / units), blocks a query can touch, B), block 256: UT threads (a unit)
+// quantise the new rows of one block of one head of K or V.  A task is 16 elements of a row, NT
+// tasks a thread, so the block's new rows stay in registers, packed as they came, between the
+// maximum and the rounding.  Bound by the bytes of the rows (64 x 1,000 tokens of 8 heads of 128:
+// 54 us, 83% of the measured copy bandwidth; unpacked to fp32 at once it held a third of the CTAs
+// and took 97).  set_len: write the new cache_len here (start given: no CTA reads cache_len).
+template <typename T, int D, int FMT, int NT, int UT>
+__global__ void __launch_bounds__(256, sizeof(T) * NT <= 4 ? 6 : 3)
 cache8_append_kernel(AppendArgs a, int set_len) {
   constexpr int CPR = D / 16;
   __shared__ uint32_t red[8];
   griddep_wait();
   griddep_launch();
-  const int h = blockIdx.x >> 1, which = blockIdx.x & 1, b = blockIdx.z;
+  // unit 2 h + which; the CTA's last units may lie past the heads and then only take the barriers
+  const int tid = threadIdx.x % UT, unit = blockIdx.x * (256 / UT) + threadIdx.x / UT;
+  const bool on = unit < 2 * a.H_kv;
+  const int h = on ? unit >> 1 : 0, which = unit & 1, b = blockIdx.z;
   const bool first = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
   AppendRange r;
   if (!append_range(a.start, a.cache_len, a.n_tokens, b, a.tokens, a.cap, first, r)) return;
@@ -227,7 +233,7 @@ cache8_append_kernel(AppendArgs a, int set_len) {
   const int blk = r.start / a.bl + blockIdx.y;
   const int x0 = blk * a.bl;  // first row of the block
   if (x0 >= end) return;
-  const int lo = max(x0, r.start), hi = min(x0 + a.bl, end);  // new rows [lo, hi)
+  const int lo = max(x0, r.start), hi = on ? min(x0 + a.bl, end) : lo;  // new rows [lo, hi)
   const T *src = static_cast<const T *>(which ? a.V : a.K) + b * (which ? a.vb : a.kb) +
                  static_cast<int64_t>(h) * D;
   const int64_t ts = which ? a.vt : a.kt;
@@ -238,13 +244,13 @@ cache8_append_kernel(AppendArgs a, int set_len) {
   uint32_t top = 0;
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const int task = threadIdx.x + 256 * u, row = x0 + task / CPR;
+    const int task = tid + UT * u, row = x0 + task / CPR;
     if (row >= lo && row < hi) v[u].load(src + (row - r.start) * ts + (task % CPR) * 16);
   }
   const float s_old = lo > x0 ? *scale : 0.0f;
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const int row = x0 + (threadIdx.x + 256 * u) / CPR;
+    const int row = x0 + (tid + UT * u) / CPR;
     if (row >= lo && row < hi) top = max(top, v[u].amax_bits());
   }
   auto cta_max = [&](uint32_t m) {
@@ -252,16 +258,17 @@ cache8_append_kernel(AppendArgs a, int set_len) {
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = m;
     __syncthreads();  // (every thread has read the old scale, too)
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = max(m, red[w]);
+    for (int w = 0; w < UT / 32; ++w) m = max(m, red[threadIdx.x / UT * (UT / 32) + w]);
     return m;
   };
   top = cta_max(top);
   const bool finite = top < kInfBits;
-  if (!finite) {  // the largest finite magnitude
+  // the largest finite magnitude (units that share a CTA take the barrier together)
+  if (UT == 256 ? !finite : __syncthreads_or(!finite) != 0) {
     top = 0;
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      const int row = x0 + (threadIdx.x + 256 * u) / CPR;
+      const int row = x0 + (tid + UT * u) / CPR;
       if (row >= lo && row < hi) {
         float x[16];
         v[u].get(x);
@@ -274,10 +281,11 @@ cache8_append_kernel(AppendArgs a, int set_len) {
   }
   const float s = fmaxf(block_scale<FMT>(__uint_as_float(top)), s_old);
   const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-  if (threadIdx.x == 0 && (s != s_old || lo == x0)) *scale = s;
+  if (!on) return;
+  if (tid == 0 && (s != s_old || lo == x0)) *scale = s;
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const int task = threadIdx.x + 256 * u, row = x0 + task / CPR;
+    const int task = tid + UT * u, row = x0 + task / CPR;
     uint4 *p = reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(task) * 16);
     if (row >= lo && row < hi) {
       float x[16];
@@ -290,7 +298,7 @@ cache8_append_kernel(AppendArgs a, int set_len) {
     }
   }
   if (a.weights && which == 0)
-    for (int x = lo + threadIdx.x; x < hi; x += 256) a.weights[bh * a.cap + x] = 0.0f;
+    for (int x = lo + tid; x < hi; x += UT) a.weights[bh * a.cap + x] = 0.0f;
 }
 
 // cache_len after an append at cache_len (start NULL): every CTA of the append has read it.

@@ -661,6 +661,18 @@ cache8_attend_kernel(Attend8Args a) {
 // Memories of fp32: CUDA cores, four columns a CTA.  Scores with a lane on each of 32 context
 // rows, outputs with a lane on D / 32 elements; sums in fp32.
 constexpr int kC8Cols32 = 4;
+// acc + sum of 16 products, one factor from shared memory (16-byte aligned)
+__device__ __forceinline__ float dot16(const float *q, const float x[16], float acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 y = *reinterpret_cast<const float4 *>(q + 4 * i);
+    acc = fmaf(y.x, x[4 * i], acc);
+    acc = fmaf(y.y, x[4 * i + 1], acc);
+    acc = fmaf(y.z, x[4 * i + 2], acc);
+    acc = fmaf(y.w, x[4 * i + 3], acc);
+  }
+  return acc;
+}
 template <int D>
 struct Attend8Smem32 {
   static constexpr int kQ = 0;
@@ -730,9 +742,7 @@ cache8_attend_f32_kernel(Attend8Args a) {
           float kx[16];
           unpack16<FMT>(*reinterpret_cast<const uint4 *>(kr + 16 * p), sc, kx);
 #pragma unroll
-          for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[c] = fmaf(qs[c * D + 16 * p + e], kx[e], s[c]);
+          for (int c = 0; c < C; ++c) s[c] = dot16(qs + c * D + 16 * p, kx, s[c]);
         }
       } else {
         const float *kr = static_cast<const float *>(a.content) + static_cast<int64_t>(table[x]) * 2 * kv + g * D;
@@ -761,32 +771,40 @@ cache8_attend_f32_kernel(Attend8Args a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[c][e] *= f[c];
     }
-    const int cnt = min(32, lim - x0);
-    for (int r = 0; r < cnt; ++r) {
-      float vx[4];
-      if (loc) {
-        const int64_t row = bh * a.cap + x0 + r;
-        const float sc = a.vs[bh * (a.cap / a.bl) + (x0 + r) / a.bl];
-        uint32_t w;
-        if constexpr (E == 4)
-          w = *reinterpret_cast<const uint32_t *>(a.v8 + row * D + 4 * lane);
-        else
-          w = *reinterpret_cast<const uint16_t *>(a.v8 + row * D + 2 * lane);
-        Fmt8<FMT>::unpack4(w, vx);
+    // eight rows of V in flight; rows past the last one have weight 0 and read the last one
+    const int last = lim - 1 - x0;
+    for (int r0 = 0; r0 <= min(31, last); r0 += 8) {
+      float v[8][4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) vx[e] *= sc;
-      } else {
-        const float *vr = static_cast<const float *>(a.content) +
-                          static_cast<int64_t>(table[x0 + r]) * 2 * kv + kv + g * D + E * lane;
+      for (int u = 0; u < 8; ++u) {
+        const int r = x0 + min(r0 + u, last);
+        if (loc) {
+          const uint8_t *vr = a.v8 + (bh * a.cap + r) * D + E * lane;
+          const float sc = a.vs[(bh * a.cap + r) >> a.bl_shift];
+          uint32_t w;
+          if constexpr (E == 4)
+            w = *reinterpret_cast<const uint32_t *>(vr);
+          else
+            w = *reinterpret_cast<const uint16_t *>(vr);
+          Fmt8<FMT>::unpack4(w, v[u]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) vx[e] = vr[e];
+          for (int e = 0; e < E; ++e) v[u][e] *= sc;
+        } else {
+          const float *vr = static_cast<const float *>(a.content) +
+                            static_cast<int64_t>(table[r]) * 2 * kv + kv + g * D + E * lane;
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[u][e] = vr[e];
+        }
       }
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float p = __shfl_sync(0xffffffffu, s[c], r);
+      for (int u = 0; u < 8; ++u)
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[c][e] = fmaf(p, vx[e], acc[c][e]);
-      }
+        for (int c = 0; c < C; ++c) {
+          float p = __shfl_sync(0xffffffffu, s[c], r0 + u);
+          if (r0 + u > last) p = 0.0f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[c][e] = fmaf(p, v[u][e], acc[c][e]);
+        }
     }
   }
   float *merge = reinterpret_cast<float *>(sm + Sm::kMerge);
@@ -806,61 +824,80 @@ cache8_attend_f32_kernel(Attend8Args a) {
 }
 
 // ---------------------------------------------------------------- combine
-// grid (B * T * H_q), block D: merge the context splits (at most kC8MaxSplit).  One warp turns the
-// splits' references and sums into factors, then a thread an element adds the parts.
+// grid ceil(rows / 4), block 128: merge the context splits (at most kC8MaxSplit), a warp a row of
+// O (token, head), a lane D / 32 elements.
 constexpr int kC8MaxSplit = 128;
-template <typename T>
+template <typename T, int D>
 __global__ void __launch_bounds__(128)
-cache8_combine_kernel(Attend8Args a, int D) {
-  __shared__ float f[kC8MaxSplit];
-  __shared__ float total;
+cache8_combine_kernel(Attend8Args a, int rows) {
+  constexpr int E = D / 32;
   griddep_wait();
   griddep_launch();
-  const int64_t row = blockIdx.x;
+  const int row = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (row >= rows) return;
   const int H_q = a.H_kv * a.G;
-  const int b = static_cast<int>(row / H_q / a.T), t = static_cast<int>(row / H_q % a.T);
+  const int b = row / H_q / a.T, t = row / H_q % a.T;
   const Attend8Query q = attend8_query(a, b, false);
   if (t >= q.n) return;
   const int n = a.n_split;
-  if (threadIdx.x < 32) {
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + row * n;
-    float2 x[kC8MaxSplit / 32];
-    float M = -INFINITY, L = 0.0f;
+  const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + static_cast<int64_t>(row) * n;
+  const float *part = a.part_o + static_cast<int64_t>(row) * n * D + lane * E;
+  float2 x[kC8MaxSplit / 32];
+  float M = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kC8MaxSplit / 32; ++i) {
-      const int s = threadIdx.x + 32 * i;
-      x[i] = s < n ? ml[s] : make_float2(-INFINITY, 0.0f);
-      M = fmaxf(M, x[i].x);
-    }
-    M = warp_max(M);
-    const float base = M == -INFINITY ? 0.0f : M;
+  for (int i = 0; i < kC8MaxSplit / 32; ++i) {
+    x[i] = lane + 32 * i < n ? ml[lane + 32 * i] : make_float2(-INFINITY, 0.0f);
+    M = fmaxf(M, x[i].x);
+  }
+  M = warp_max(M);
+  const float base = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f, o[E];
 #pragma unroll
-    for (int i = 0; i < kC8MaxSplit / 32; ++i) {
-      const float e = exp2f(x[i].x - base);
-      f[threadIdx.x + 32 * i] = e;
-      L += x[i].y * e;
-    }
-    L = warp_sum(L);
-    if (threadIdx.x == 0) {
-      total = L;
-      if (a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kC8MaxSplit / 32; ++i) {
+    if (32 * i >= n) break;
+    const float f = exp2f(x[i].x - base);
+    L += x[i].y * f;
+    const int m = min(32, n - 32 * i);
+#pragma unroll 8
+    for (int s = 0; s < m; ++s) {
+      const float fs = __shfl_sync(0xffffffffu, f, s);
+      const float *p = part + static_cast<int64_t>(32 * i + s) * D;
+      if constexpr (E == 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(p);
+        o[0] = fmaf(y.x, fs, o[0]);
+        o[1] = fmaf(y.y, fs, o[1]);
+        o[2] = fmaf(y.z, fs, o[2]);
+        o[3] = fmaf(y.w, fs, o[3]);
+      } else {
+        const float2 y = *reinterpret_cast<const float2 *>(p);
+        o[0] = fmaf(y.x, fs, o[0]);
+        o[1] = fmaf(y.y, fs, o[1]);
+      }
     }
   }
-  __syncthreads();
-  const float *part = a.part_o + row * n * D + threadIdx.x;
-  float o = 0.0f;
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) o = fmaf(part[static_cast<int64_t>(s) * D], f[s], o);
-  static_cast<T *>(a.O)[row * D + threadIdx.x] = Elem<T>::from_f(total == 0.0f ? 0.0f : o / total);
+  L = warp_sum(L);
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = L == 0.0f ? 0.0f : o[e] / L;
+  T *out = static_cast<T *>(a.O) + static_cast<int64_t>(row) * D + lane * E;
+  if constexpr (E == 4) {
+    store4(out, o);
+  } else {
+    out[0] = Elem<T>::from_f(o[0]);
+    out[1] = Elem<T>::from_f(o[1]);
+  }
+  if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
 }
 
 // ---------------------------------------------------------------- weights
 // The weight each cached row received: with the softmax's log-sum known, a second pass over K
-// alone recomputes the scores, p = 2^(s - lse), and sums them over the columns.  A CTA copies
-// kC8wRows rows to shared memory once and walks over all columns, 8 NT at a time with Q's fragments
-// in registers; a warp's tiles keep their sums in registers.  Few columns: bound by K's bytes.
-// grid (ceil(cap / kC8wRows), B * H_kv), block 32 * kC8Warps.  fp32 memories: see below.
-constexpr int kC8wTiles = 4;                              // 16-row tiles a warp
+// alone recomputes the scores, p = 2^(s - lse), and sums them over the columns, 8 NT at a time with
+// Q's fragments in registers.  Few columns (one round of 8 NT): bound by K's bytes; a warp streams
+// its tiles through a ring.  More: a CTA copies kC8wRows rows to shared memory once and walks over
+// all columns, its tiles' sums in registers.
+// grid (CTAs a head, B * H_kv), block 32 * kC8Warps.  fp32 memories: see below.
+constexpr int kC8wTiles = 4;                              // 16-row tiles a warp, or its ring
 constexpr int kC8wRows = 16 * kC8wTiles * kC8Warps;
 template <int D, int NT>
 struct Weight8Smem {
@@ -868,45 +905,20 @@ struct Weight8Smem {
   static constexpr int kLse = kK + kC8wRows * D;
   static constexpr int kBytes = kLse + 8 * NT * 4;
 };
+
+// Columns [c0, c0 + 8 NT) as a lane holds them, and the weights they give a tile's rows.
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(32 * kC8Warps)
-cache8_weight_kernel(Attend8Args a) {
-  using Sm = Attend8Smem<D, NT>;
-  using Wm = Weight8Smem<D, NT>;
-  constexpr int KS = D / 16;
-  extern __shared__ __align__(16) uint8_t sm[];
-  float *lse2 = reinterpret_cast<float *>(sm + Wm::kLse);
-  griddep_wait();
-  griddep_launch();
-  const int b = blockIdx.y / a.H_kv, g = blockIdx.y % a.H_kv;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, lg = lane >> 2, lt = lane & 3;
-  const Attend8Query q = attend8_query(a, b, false);
-  const int r0 = blockIdx.x * kC8wRows;
-  if (r0 >= q.len) return;
-  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
-  // tile i of this warp: rows r0 + 16 (kC8Warps i + warp) ..
-  auto tile_row = [&](int i) { return r0 + 16 * (kC8Warps * i + warp); };
-  const uint32_t ring = smem_u32(sm + Wm::kK) + warp * kC8wTiles * Tile8<D>::kBytes;
-  float k_scale[kC8wTiles], sum[kC8wTiles][2];
-#pragma unroll
-  for (int i = 0; i < kC8wTiles; ++i) {
-    const int x0 = tile_row(i);
-    k_scale[i] = sum[i][0] = sum[i][1] = 0.0f;
-    if (x0 < q.len) {
-      const uint8_t *src = a.k8 + (bh * a.cap + x0) * D;
-#pragma unroll
-      for (int u = 0; u < D / 32; ++u) {
-        const int p = lane + 32 * u;
-        cp_async_16(ring + i * Tile8<D>::kBytes + Tile8<D>::k_off(p / (D / 16), p % (D / 16)), src + 16 * p, true);
-      }
-      k_scale[i] = a.ks[(bh * a.cap + x0) >> a.bl_shift];
-    }
-  }
-  cp_async_commit();
-  const __half *qh = reinterpret_cast<const __half *>(sm + Sm::kQ);
-  const float *cs = reinterpret_cast<const float *>(sm + Sm::kColScale);
-  for (int c0 = 0; c0 < q.n * a.G; c0 += Sm::kCols) {
-    if (c0) __syncthreads();
+struct WeightColumns {
+  static constexpr int KS = D / 16;
+  uint32_t qf[NT][KS][2];
+  float cf[NT][2], ls[NT][2];
+  int rows[NT][2], all_see;
+
+  // Q, its scales and the log-sums to shared memory and from there to registers (all warps)
+  __device__ __forceinline__ void load(const Attend8Args &a, const Attend8Query &q, int b, int g,
+                                       int c0, uint8_t *sm, float *lse2) {
+    using Sm = Attend8Smem<D, NT>;
+    const int lane = threadIdx.x % 32, lg = lane >> 2, lt = lane & 3;
     load_q_columns<D, NT>(a, b, g, c0, q.n, sm);
     for (int c = threadIdx.x; c < Sm::kCols; c += 32 * kC8Warps) {
       const int cc = c0 + c, t = col_token(a, cc);
@@ -917,12 +929,10 @@ cache8_weight_kernel(Attend8Args a) {
       }
       lse2[c] = v;
     }
-    cp_async_wait<0>();
     __syncthreads();
-    const int all_see = column_rows(a, q, c0);  // rows that every column of this round sees
-    uint32_t qf[NT][KS][2];
-    float cf[NT][2], ls[NT][2];
-    int rows[NT][2];
+    const __half *qh = reinterpret_cast<const __half *>(sm + Sm::kQ);
+    const float *cs = reinterpret_cast<const float *>(sm + Sm::kColScale);
+    all_see = column_rows(a, q, c0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -939,50 +949,126 @@ cache8_weight_kernel(Attend8Args a) {
         rows[nt][h] = column_rows(a, q, c0 + c);
       }
     }
-#pragma unroll
-    for (int i = 0; i < kC8wTiles; ++i) {
-      const int x0 = tile_row(i);
-      if (x0 >= q.len) break;
-      KTile<D> kt;
-      kt.from_shared(ring + i * Tile8<D>::kBytes, lane);
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t a0, a1, a2, a3;
-        widen4<FMT>(kt.w[0][k], a0, a2);
-        widen4<FMT>(kt.w[1][k], a1, a3);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
-      }
-      const bool masked = x0 + 16 > all_see;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p = ex2_approx(s[nt][e] * (cf[nt][e & 1] * k_scale[i]) - ls[nt][e & 1]);
-          if (masked && x0 + lg + 8 * (e >> 1) >= rows[nt][e & 1]) p = 0.0f;
-          sum[i][e >> 1] += p;
-        }
-    }
   }
-  cp_async_wait<0>();
+  // this lane's part of the weights of rows x0 + g and x0 + g + 8
+  __device__ __forceinline__ void add(uint32_t stage, int x0, float k_scale, float (&sum)[2]) const {
+    const int lane = threadIdx.x % 32, lg = lane >> 2;
+    KTile<D> kt;
+    kt.from_shared(stage, lane);
+    float s[NT][4];
 #pragma unroll
-  for (int i = 0; i < kC8wTiles; ++i)
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      uint32_t a0, a1, a2, a3;
+      widen4<FMT>(kt.w[0][k], a0, a2);
+      widen4<FMT>(kt.w[1][k], a1, a3);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
+    }
+    const bool masked = x0 + 16 > all_see;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float p = ex2_approx(s[nt][e] * (cf[nt][e & 1] * k_scale) - ls[nt][e & 1]);
+        if (masked && x0 + lg + 8 * (e >> 1) >= rows[nt][e & 1]) p = 0.0f;
+        sum[e >> 1] += p;
+      }
+  }
+};
+
+template <int D, int NT, int FMT>
+__global__ void __launch_bounds__(32 * kC8Warps)
+cache8_weight_kernel(Attend8Args a, int stream) {
+  using Wm = Weight8Smem<D, NT>;
+  extern __shared__ __align__(16) uint8_t sm[];
+  float *lse2 = reinterpret_cast<float *>(sm + Wm::kLse);
+  griddep_wait();
+  griddep_launch();
+  const int b = blockIdx.y / a.H_kv, g = blockIdx.y % a.H_kv;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const Attend8Query q = attend8_query(a, b, false);
+  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
+  const int tiles = (q.len + 15) / 16, cols = q.n * a.G;
+  const uint32_t ring = smem_u32(sm + Wm::kK) + warp * kC8wTiles * Tile8<D>::kBytes;
+  WeightColumns<D, NT, FMT> col;
+  auto fetch = [&](int slot, int tile) {
+    const uint8_t *src = a.k8 + (bh * a.cap + tile * 16) * D;
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      const int p = lane + 32 * u;
+      cp_async_16(ring + slot * Tile8<D>::kBytes + Tile8<D>::k_off(p / (D / 16), p % (D / 16)), src + 16 * p, true);
+    }
+  };
+  auto scale_of = [&](int tile) { return a.ks[(bh * a.cap + tile * 16) >> a.bl_shift]; };
+  auto write = [&](int tile, const float (&sum)[2]) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float x = sum[i][r];
+      float x = sum[r];
       x += __shfl_xor_sync(0xffffffffu, x, 1);
       x += __shfl_xor_sync(0xffffffffu, x, 2);
-      const int row = tile_row(i) + lg + 8 * r;
-      if (lt == 0 && row < q.len) {
+      const int row = tile * 16 + (lane >> 2) + 8 * r;
+      if ((lane & 3) == 0 && row < q.len) {
         float *w = a.weights + bh * a.cap + row;
         *w = a.decay == 0.0f ? x : a.decay * *w + x;
       }
     }
+  };
+  if (stream) {
+    const int step = gridDim.x * kC8Warps;
+    int tile = blockIdx.x * kC8Warps + warp, ahead = tile;
+#pragma unroll
+    for (int i = 0; i < kC8wTiles - 1; ++i) {
+      if (ahead < tiles) fetch(i, ahead);
+      cp_async_commit();
+      ahead += step;
+    }
+    col.load(a, q, b, g, 0, sm, lse2);
+    float k_scale = tile < tiles ? scale_of(tile) : 0.0f;
+    for (int slot = 0; tile < tiles; tile += step) {
+      cp_async_wait<kC8wTiles - 2>();
+      __syncwarp();  // every lane's copies are there; the slot of the last tile is free
+      if (ahead < tiles) fetch((slot + kC8wTiles - 1) % kC8wTiles, ahead);
+      cp_async_commit();
+      ahead += step;
+      const float ks = k_scale;
+      if (tile + step < tiles) k_scale = scale_of(tile + step);
+      float sum[2] = {0.0f, 0.0f};
+      if (cols > 0) col.add(ring + slot * Tile8<D>::kBytes, tile * 16, ks, sum);
+      write(tile, sum);
+      slot = (slot + 1) % kC8wTiles;
+    }
+    cp_async_wait<0>();
+    return;
+  }
+  if (static_cast<int>(blockIdx.x) * kC8wRows >= q.len) return;
+  // tile i of this warp
+  auto tile_of = [&](int i) { return blockIdx.x * (kC8wRows / 16) + kC8Warps * i + warp; };
+  float k_scale[kC8wTiles], sum[kC8wTiles][2];
+#pragma unroll
+  for (int i = 0; i < kC8wTiles; ++i) {
+    k_scale[i] = sum[i][0] = sum[i][1] = 0.0f;
+    if (tile_of(i) < tiles) {
+      fetch(i, tile_of(i));
+      k_scale[i] = scale_of(tile_of(i));
+    }
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncwarp();
+  for (int c0 = 0; c0 < cols; c0 += 8 * NT) {
+    if (c0) __syncthreads();
+    col.load(a, q, b, g, c0, sm, lse2);
+#pragma unroll
+    for (int i = 0; i < kC8wTiles; ++i)
+      if (tile_of(i) < tiles) col.add(ring + i * Tile8<D>::kBytes, tile_of(i) * 16, k_scale[i], sum[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kC8wTiles; ++i)
+    if (tile_of(i) < tiles) write(tile_of(i), sum[i]);
 }
 
 // The same on CUDA cores: a lane on each of 32 rows, Q broadcast from shared memory.
@@ -1022,9 +1108,7 @@ cache8_weight_f32_kernel(Attend8Args a) {
       float kx[16];
       unpack16<FMT>(*reinterpret_cast<const uint4 *>(kr + 16 * p), sc, kx);
 #pragma unroll
-      for (int c = 0; c < kC8Cols32; ++c)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[c] = fmaf(qs[c * D + 16 * p + e], kx[e], s[c]);
+      for (int c = 0; c < kC8Cols32; ++c) s[c] = dot16(qs + c * D + 16 * p, kx, s[c]);
     }
 #pragma unroll
     for (int c = 0; c < kC8Cols32; ++c)

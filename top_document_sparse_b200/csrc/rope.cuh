@@ -28,57 +28,61 @@ struct alignas(sizeof(T) * V) RopeVec {
   T v[V];
 };
 
-// One task: V elements of a rotated half (with their V partners), V / 2
-// interleaved pairs, or V elements of the rest of the head.
+// One task: V elements of a rotated half with their V partners, V interleaved elements (one pair
+// for V = 1, moved by scalar loads: rows without alignment), or V elements of the rest of the head.
 template <typename T, int V, bool INTER>
-__device__ __forceinline__ void rope_task(const T *in, T *out, int task, int rot_tasks, int r,
-                                          const float2 *cs) {
+struct RopeTask {
+  static constexpr int N = INTER && V == 1 ? 2 : V;
   using Vec = RopeVec<T, V>;
-  if (task >= rot_tasks) {
-    const int e = r + (task - rot_tasks) * V;
-    *reinterpret_cast<Vec *>(out + e) = *reinterpret_cast<const Vec *>(in + e);
-    return;
-  }
-  if constexpr (INTER) {
-    // V = 1 stands for one pair moved by scalar loads (rows without alignment)
-    constexpr int N = V == 1 ? 2 : V;
-    const int e = task * N;
-    T x[N], y[N];
-    if constexpr (V == 1) {
+  T x[2 * N];  // interleaved: N elements
+  T *out;
+  const float2 *cs;
+  int e;       // first element
+  bool rot;
+
+  __device__ __forceinline__ void load(const T *in, T *o, int task, int rot_tasks, int r,
+                                       const float2 *token_cs) {
+    rot = task < rot_tasks;
+    e = rot ? task * N : r + (task - rot_tasks) * V;
+    out = o + e;
+    cs = token_cs;
+    if constexpr (INTER && V == 1) {
       x[0] = in[e];
-      x[1] = in[e + 1];
+      if (rot) x[1] = in[e + 1];
     } else {
       *reinterpret_cast<Vec *>(x) = *reinterpret_cast<const Vec *>(in + e);
+      if (!INTER && rot) *reinterpret_cast<Vec *>(x + N) = *reinterpret_cast<const Vec *>(in + e + (r >> 1));
     }
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float2 c = cs[(e + i) >> 1];
-      const float a = Elem<T>::to_f(x[i]), b = Elem<T>::to_f(x[i + 1]);
-      y[i] = Elem<T>::from_f(a * c.x - b * c.y);
-      y[i + 1] = Elem<T>::from_f(b * c.x + a * c.y);
-    }
-    if constexpr (V == 1) {
-      out[e] = y[0];
-      out[e + 1] = y[1];
-    } else {
-      *reinterpret_cast<Vec *>(out + e) = *reinterpret_cast<const Vec *>(y);
-    }
-  } else {
-    const int e = task * V, half = r >> 1;
-    const Vec xa = *reinterpret_cast<const Vec *>(in + e);
-    const Vec xb = *reinterpret_cast<const Vec *>(in + e + half);
-    Vec ya, yb;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 c = cs[e + i];
-      const float a = Elem<T>::to_f(xa.v[i]), b = Elem<T>::to_f(xb.v[i]);
-      ya.v[i] = Elem<T>::from_f(a * c.x - b * c.y);
-      yb.v[i] = Elem<T>::from_f(b * c.x + a * c.y);
-    }
-    *reinterpret_cast<Vec *>(out + e) = ya;
-    *reinterpret_cast<Vec *>(out + e + half) = yb;
   }
-}
+  __device__ __forceinline__ void store(int r) {
+    if constexpr (INTER) {
+      if (rot) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const float2 c = cs[(e + i) >> 1];
+          const float a = Elem<T>::to_f(x[i]), b = Elem<T>::to_f(x[i + 1]);
+          x[i] = Elem<T>::from_f(a * c.x - b * c.y);
+          x[i + 1] = Elem<T>::from_f(b * c.x + a * c.y);
+        }
+      }
+    } else if (rot) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float2 c = cs[e + i];
+        const float a = Elem<T>::to_f(x[i]), b = Elem<T>::to_f(x[N + i]);
+        x[i] = Elem<T>::from_f(a * c.x - b * c.y);
+        x[N + i] = Elem<T>::from_f(b * c.x + a * c.y);
+      }
+    }
+    if constexpr (INTER && V == 1) {
+      out[0] = x[0];
+      if (rot) out[1] = x[1];
+    } else {
+      *reinterpret_cast<Vec *>(out) = *reinterpret_cast<const Vec *>(x);
+      if (!INTER && rot) *reinterpret_cast<Vec *>(out + (r >> 1)) = *reinterpret_cast<const Vec *>(x + N);
+    }
+  }
+};
 
 // grid ceil(tokens / tok_cta), block <= kRopeThreads, shared tok_cta * r / 2 float2.
 // per_head = rot_tasks + the tasks of the copied rest (0 where the rest stays
@@ -94,25 +98,36 @@ rope_kernel(const uint64_t *__restrict__ freq, int r, int D, float magnitude, in
   const int half = r >> 1;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok_cta;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tok_cta), tokens - t0));
-  for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
-    const int t = i / half, p = i - t * half;
+  const int per_token = (q.heads + k.heads) * per_head;
+  const int total = nt * per_token;
+  using Task = RopeTask<T, V, INTER>;
+  auto load = [&](Task &task, int i) {
+    const int t = i / per_token, j = i - t * per_token;
+    const int h = j / per_head;
+    const bool is_q = h < q.heads;
+    const RopeSide &s = is_q ? q : k;
+    const int hh = is_q ? h : h - q.heads;
+    task.load(static_cast<const T *>(s.in) + (t0 + t) * s.in_stride + hh * D,
+              static_cast<T *>(s.out) + (t0 + t) * s.out_stride + hh * D, j - h * per_head, rot_tasks, r,
+              rope_cs + t * half);
+  };
+  // a thread's first elements are under way while the angles are computed
+  Task task;
+  int i = threadIdx.x;
+  if (i < total) load(task, i);
+  for (int a = threadIdx.x; a < nt * half; a += blockDim.x) {
+    const int t = a / half, p = a - t * half;
     const uint64_t turn = static_cast<uint64_t>(positions[t0 + t]) * freq[p];
     float s, c;
     // the signed top half is the angle in units of 2^-32 turns, within half a turn
     sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
-    rope_cs[i] = make_float2(c * magnitude, (inverse ? -s : s) * magnitude);
+    rope_cs[a] = make_float2(c * magnitude, (inverse ? -s : s) * magnitude);
   }
   __syncthreads();
-  const int per_token = (q.heads + k.heads) * per_head;
-  for (int i = threadIdx.x; i < nt * per_token; i += blockDim.x) {
-    const int t = i / per_token, j = i - t * per_token;
-    const int h = j / per_head, task = j - h * per_head;
-    const bool is_q = h < q.heads;
-    const RopeSide &s = is_q ? q : k;
-    const int hh = is_q ? h : h - q.heads;
-    const T *in = static_cast<const T *>(s.in) + (t0 + t) * s.in_stride + hh * D;
-    T *out = static_cast<T *>(s.out) + (t0 + t) * s.out_stride + hh * D;
-    rope_task<T, V, INTER>(in, out, task, rot_tasks, r, rope_cs + t * half);
+  while (i < total) {
+    task.store(r);
+    i += blockDim.x;
+    if (i < total) load(task, i);
   }
 }
 

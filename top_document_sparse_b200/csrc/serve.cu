@@ -2,7 +2,10 @@
 // 8-bit local cache: host-side validation and launches.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 #include <new>
+#include <type_traits>
+#include <utility>
 #include <vector>
 
 #include "host.cuh"
@@ -36,6 +39,34 @@ cudaError_t take_serve_error(unsigned int *bits, cudaStream_t st) {
 namespace {
 
 cudaStream_t to_stream(msa_stream s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// Let `kern` use `bytes` of dynamic shared memory.  The attribute is set when it first has to grow
+// on a device and remembered, not set at every call.
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes) {
+  struct Known {
+    const void *kern;
+    int device, bytes;
+  };
+  static std::mutex mu;
+  static Known known[256];
+  static int n = 0;
+  if (bytes <= 48 * 1024) return cudaSuccess;  // no opt-in needed
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const void *key = reinterpret_cast<const void *>(kern);
+  std::lock_guard<std::mutex> lock(mu);
+  Known *k = nullptr;
+  for (int i = 0; i < n; ++i)
+    if (known[i].kern == key && known[i].device == dev) k = &known[i];
+  if (k && k->bytes >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  if (!k && n < 256) k = &(known[n++] = Known{key, dev, 0});
+  if (k) k->bytes = bytes;
+  return cudaSuccess;
+}
 
 // ---------------------------------------------------------------- rotary positions
 msa_status rope_frequencies(const msa_rope_config *c, std::vector<uint64_t> &freq, float *magnitude) {
@@ -76,12 +107,13 @@ msa_status launch_rope(const msa_rope *rope, int64_t tokens, const int64_t *pos,
   const int rot = (V == 1 || !INTER) ? half / V : rope->r / V;
   const int rest = copy_rest ? (rope->D - rope->r) / V : 0;
   // tokens a CTA: enough tasks for every thread
-  // one task a thread where a token's tasks fit a block, so that no round runs half empty (40 heads
-  // of 128: 320 threads, 70 -> XX us against blocks of 256 for 16,384 tokens)
+  // Small CTAs overlap one another's angles and copies best: 16,384 tokens of 40 heads of 128 take
+  // 60 us at 64 threads, 64 at 128, 66 at 160, 68 to 84 at 256.  With few tokens a thread a task is
+  // faster (64 tokens: 2.1 us at 320 threads, 3.8 at 64).
   const int per_token = (q.heads + k.heads) * (rot + rest);
-  const int tok = std::max(1, std::min(16, 256 / std::max(per_token, 1)));
-  const int rounds = (tok * per_token + msa::kRopeThreads - 1) / msa::kRopeThreads;
-  const int threads = round32((tok * per_token + rounds - 1) / rounds);
+  const bool few = tokens * round32(per_token) < 2048LL * num_sms();
+  const int tok = std::max(1, std::min(16, (few ? 256 : 64) / std::max(per_token, 1)));
+  const int threads = few ? std::min(round32(tok * per_token), msa::kRopeThreads) : 64;
   const int64_t grid = (tokens + tok - 1) / tok;
   if (grid > 0x7FFFFFFF) return fail(MSA_ERR_UNSUPPORTED, "too many tokens");
   MSA_CUDA(launch_pdl(msa::rope_kernel<T, V, INTER>, dim3(static_cast<unsigned>(grid)),
@@ -141,10 +173,13 @@ msa_status launch_append(const msa::AppendArgs &a, int B, bool set_len, cudaStre
   const int blocks = static_cast<int>(
       std::min<int64_t>((static_cast<int64_t>(a.tokens) + a.bl - 2) / a.bl + 1, a.cap / a.bl + 1));
   if (blocks > 65535) return fail(MSA_ERR_UNSUPPORTED, "too many tokens for one append");
-  const dim3 grid(2 * a.H_kv, blocks, B);
-  auto kern = tasks <= 256   ? msa::cache8_append_kernel<T, D, FMT, 1>
-              : tasks == 512 ? msa::cache8_append_kernel<T, D, FMT, 2>
-                             : msa::cache8_append_kernel<T, D, FMT, 4>;
+  const int units = std::max(1, 256 / tasks);  // (head, K or V) pairs a CTA
+  const dim3 grid((2 * a.H_kv + units - 1) / units, blocks, B);
+  auto kern = tasks == 64    ? msa::cache8_append_kernel<T, D, FMT, 1, 64>
+              : tasks == 128 ? msa::cache8_append_kernel<T, D, FMT, 1, 128>
+              : tasks == 256 ? msa::cache8_append_kernel<T, D, FMT, 1, 256>
+              : tasks == 512 ? msa::cache8_append_kernel<T, D, FMT, 2, 256>
+                             : msa::cache8_append_kernel<T, D, FMT, 4, 256>;
   MSA_CUDA(launch_pdl(kern, grid, dim3(256), 0, st, a, set_len ? 1 : 0));
   MSA_LAUNCHED("cache8_append_kernel");
   if (!set_len) {
@@ -240,19 +275,24 @@ Attend8Plan plan_attend8(const msa_memory *mem, const msa_cache8 *c, int T, int 
                                          : msa::kC8Cols32;
   p.col_tiles = static_cast<int>((cols + per - 1) / per);
   const int64_t ctas = bh * p.col_tiles;
-  const int64_t want = 3LL * num_sms();
-  // Splits of at most 2,048 local rows, so that ragged lengths spread over the SMs, and enough of
-  // them for three CTAs an SM (64 queries of up to 8,192 rows: 133 us at 4,096 rows a split, 124
-  // at 2,048, 131 at 1,024).  Where the context is split anyway, the memory rows get splits of
-  // their own, so that the others need no chunk table.
-  int64_t loc = (c->capacity + 2047) / 2048;
-  if (ctas * loc < want) loc = std::min<int64_t>((want + ctas - 1) / ctas, (c->capacity + 63) / 64);
-  loc = std::min<int64_t>(loc, 64);
-  p.n_split = p.loc_split = static_cast<int>(loc);
-  if (mem->dtype == MSA_BF16 && max_mem > 0 && (loc > 1 || ctas < want)) {
-    const int64_t own = std::min<int64_t>((max_mem + 63) / 64, std::max<int64_t>(1, want / ctas));
-    p.n_split += static_cast<int>(std::min<int64_t>(own, msa::kC8MaxSplit - 64));
+  // Splits of at most 2,048 local rows, so that ragged lengths spread over the SMs (64 queries of
+  // up to 8,192 rows: 133 us at 4,096 rows a split, 124 at 2,048, 131 at 1,024).  Fewer CTAs than
+  // fit the GPU at a time: as many splits as fill it once, down to 64 rows each.  Where the context
+  // is split, the memory rows get splits of their own, so that the others need no chunk table; a
+  // memory row counts as two local ones (bf16 against one byte).
+  const bool bf16 = mem->dtype == MSA_BF16;
+  const int64_t room = static_cast<int64_t>(num_sms()) * (!bf16 || per == 8 ? 4 : per == 16 ? 3 : 2);
+  int64_t loc = (c->capacity + 2047) / 2048, own = 0;
+  const bool fill = ctas * (loc + (max_mem > 0 ? 1 : 0)) < room;
+  if (fill) loc = std::max<int64_t>(1, room / ctas);
+  if (bf16 && max_mem > 0 && loc > 1) {
+    own = std::max<int64_t>(1, loc * 2 * max_mem / (2 * max_mem + c->capacity));
+    own = std::min<int64_t>(std::min<int64_t>(own, (max_mem + 63) / 64), msa::kC8MaxSplit - 64);
+    if (fill) loc = std::max<int64_t>(1, loc - own);
   }
+  loc = std::min<int64_t>(std::min<int64_t>(loc, (c->capacity + 63) / 64), 64);
+  p.loc_split = static_cast<int>(loc);
+  p.n_split = static_cast<int>(loc + own);
   plan_attend8_scratch(p, mem, c, rows);
   return p;
 }
@@ -278,7 +318,7 @@ template <int FMT>
 msa_status launch_prefill8(const msa::Attend8Args &a, const Attend8Plan &p, int B, cudaStream_t st) {
   auto kern = msa::cache8_prefill_tc_kernel<FMT>;
   const int smem = msa::C8tSmem::bytes(p.table_cap);
-  MSA_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  MSA_CUDA(allow_smem(kern, smem));
   const int64_t ctas = static_cast<int64_t>(B) * a.H_kv * p.col_tiles;
   if (ctas > 0x7FFFFFFF) return fail(MSA_ERR_UNSUPPORTED, "too many query tokens");
   MSA_CUDA(launch_pdl(kern, dim3(static_cast<unsigned>(ctas), p.n_split), dim3(msa::kC8tThreads), smem,
@@ -304,22 +344,27 @@ msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B
     const msa_status s = launch_prefill8<FMT>(a, p, B, st);
     if (s != MSA_OK) return s;
   } else {
-    MSA_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    MSA_CUDA(allow_smem(kern, smem));
     MSA_CUDA(launch_pdl(kern, grid, block, smem, st, a));
     MSA_LAUNCHED("cache8_attend_kernel");
   }
   if (p.n_split > 1) {
-    MSA_CUDA(launch_pdl(msa::cache8_combine_kernel<T>,
-                        dim3(static_cast<unsigned>(B * a.T * a.H_kv * a.G)), dim3(D), 0, st, a, D));
+    MSA_CUDA(launch_pdl(msa::cache8_combine_kernel<T, D>,
+                        dim3(static_cast<unsigned>((static_cast<int64_t>(B) * a.T * a.H_kv * a.G + 3) / 4)),
+                        dim3(128), 0, st, a, B * a.T * a.H_kv * a.G));
     MSA_LAUNCHED("cache8_combine_kernel");
   }
   if (a.weights) {
     if constexpr (kBf16) {
       auto wk = msa::cache8_weight_kernel<D, NT, FMT>;
       const int ws = msa::Weight8Smem<D, NT>::kBytes;
-      MSA_CUDA(cudaFuncSetAttribute(wk, cudaFuncAttributeMaxDynamicSharedMemorySize, ws));
-      MSA_CUDA(launch_pdl(wk, dim3((a.cap + msa::kC8wRows - 1) / msa::kC8wRows, B * a.H_kv), block, ws,
-                          st, a));
+      MSA_CUDA(allow_smem(wk, ws));
+      // one round of columns: a CTA streams its share of the tiles, about five CTAs an SM in all
+      // (a CTA's set-up takes as long as a dozen tiles); more rounds: a CTA for every kC8wRows rows
+      const int chunks = (a.cap + msa::kC8wRows - 1) / msa::kC8wRows;
+      const bool stream = static_cast<int64_t>(a.T) * a.G <= 8 * NT;
+      const int grid_x = stream ? std::min(chunks, (5 * num_sms() + B * a.H_kv - 1) / (B * a.H_kv)) : chunks;
+      MSA_CUDA(launch_pdl(wk, dim3(grid_x, B * a.H_kv), block, ws, st, a, stream ? 1 : 0));
     } else
       MSA_CUDA(launch_pdl(msa::cache8_weight_f32_kernel<D, FMT>,
                           dim3((a.cap + 127) / 128, B * a.H_kv), block, 0, st, a));

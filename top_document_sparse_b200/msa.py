@@ -462,32 +462,43 @@ class LayerDecode:
                              workspace_bytes=self.workspace.numel())
 
 
-def _tensor(t, name: str, shape, dtype, device, contiguous: bool = True) -> int:
-    """Check one argument of the rotary and 8-bit cache calls; its device pointer."""
+def _tensor(t, name: str, shape, dtype, index: int, contiguous: bool = True) -> int:
+    """Check one argument of the rotary and 8-bit cache calls (on device `index`); its pointer."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
 
 
+def _buffer(t, name: str, index: int):
+    """(pointer, bytes) of a workspace."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor on cuda:{index}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _call(fn, device, stream, *args):
-    """One library call on `device` (made current for it) and `stream` (default: its current one)."""
+    """One library call on `device` (made current for it) and `stream` (default: its current one).
+    The raw accessors are the ones behind torch.cuda.current_stream() and current_device(), without
+    building their objects: a small call's time is its issue."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream.cuda_stream)
+    else:
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, raw)
     if status != 0:
         _check(status)
 
@@ -542,44 +553,56 @@ class Rope:
 
     def _side(self, x, name, lead, dtype):
         """(pointer, heads, token stride) of one of Q and K."""
-        _tensor(x, name, lead + x.shape[-2:], dtype, self.device, contiguous=False)
-        H, D = x.shape[-2:]
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        shape = x.shape
+        if len(shape) < 2 or shape[:-2] != lead or shape[-1] != self.head_dim:
+            raise ValueError(f"{name}: expected shape {(*lead, 'heads', self.head_dim)}, got "
+                             f"{tuple(shape)}")
+        if x.dtype is not dtype:
+            raise ValueError(f"{name}: expected {dtype}, got {x.dtype}")
+        if x.get_device() != self.device.index:
+            raise ValueError(f"{name}: expected a tensor on {self.device}, got {x.device}")
+        H, D = shape[-2], shape[-1]
+        if x.is_contiguous():
+            return x.data_ptr(), H, H * D
         st = x.stride()
-        if D != self.head_dim:
-            raise ValueError(f"{name}: expected head_dim {self.head_dim}, got {D}")
         ok = st[-1] == 1 and (H == 1 or st[-2] == D)
-        step = H * D  # distance of consecutive tokens
-        if len(lead) and lead.numel() > 1:
-            n, step = 1, None
-            for d in range(len(lead) - 1, -1, -1):
-                if lead[d] == 1:
-                    continue
-                if step is None:
-                    step = st[d]
+        n, step = 1, None  # tokens so far, distance of consecutive ones
+        for d in range(len(lead) - 1, -1, -1):
+            if lead[d] != 1:
+                step = st[d] if step is None else step
                 ok = ok and st[d] == n * step
                 n *= lead[d]
         if not ok:
             raise ValueError(f"{name}: heads must be dense and tokens evenly spaced")
-        return x.data_ptr(), H, step
+        return x.data_ptr(), H, H * D if step is None else step
 
     def _apply(self, inverse, q, k, positions, q_out, k_out, stream):
+        if not isinstance(positions, torch.Tensor):
+            raise TypeError("positions: expected a torch.Tensor")
         lead = positions.shape
-        pos = _tensor(positions, "positions", lead, torch.int64, self.device)
+        pos = _tensor(positions, "positions", lead, torch.int64, self.device.index)
         if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE:
             raise TypeError("q: expected an fp32 or bf16 torch.Tensor")
+        dtype = q.dtype
+        qp, qh, qs = self._side(q, "q", lead, dtype)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        qp, qh, qs = self._side(q, "q", lead, q.dtype)
-        qo, qoh, qos = self._side(q_out, "q_out", lead, q.dtype)
+            q_out = torch.empty(q.shape, dtype=dtype, device=self.device)
+            qo, qoh, qos = q_out.data_ptr(), qh, qh * self.head_dim
+        else:
+            qo, qoh, qos = self._side(q_out, "q_out", lead, dtype)
         kp, kh, ks, ko, koh, kos = None, 0, 0, None, 0, 0
         if k is not None:
+            kp, kh, ks = self._side(k, "k", lead, dtype)
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            kp, kh, ks = self._side(k, "k", lead, q.dtype)
-            ko, koh, kos = self._side(k_out, "k_out", lead, q.dtype)
+                k_out = torch.empty(k.shape, dtype=dtype, device=self.device)
+                ko, koh, kos = k_out.data_ptr(), kh, kh * self.head_dim
+            else:
+                ko, koh, kos = self._side(k_out, "k_out", lead, dtype)
         if qoh != qh or koh != kh:
             raise ValueError("the outputs must have the heads of the inputs")
-        _call(_lib.msa_rope_apply, self.device, stream, self.handle, _DTYPE[q.dtype],
+        _call(_lib.msa_rope_apply, self.device, stream, self.handle, _DTYPE[dtype],
               positions.numel(), pos, inverse, qp, qh, qs, qo, qos, kp, kh, ks, ko, kos)
         return q_out, k_out
 
@@ -628,22 +651,23 @@ class Cache8:
         self._ref = ctypes.byref(self.c)
 
     def _counts(self, t, name):
-        return None if t is None else _tensor(t, name, (self.batch,), torch.int32, self.device)
+        return None if t is None else _tensor(t, name, (self.batch,), torch.int32, self.device.index)
 
     def append(self, K, V, n_tokens=None, start=None, stream=None):
         """Append [batch][tokens][H_kv][D] rows, K already rotated (msa_cache8_append).  K and V
         may be slices of a joint projection (H_kv and D dense, rows on 16 bytes)."""
         mem = self.mem
-        if K.dim() != 4:
+        if not isinstance(K, torch.Tensor) or K.dim() != 4:
             raise ValueError("K: expected [batch][tokens][H_kv][D]")
         T = K.shape[1]
         shape = (self.batch, T, mem.n_kv_heads, mem.head_dim)
-        kp = _tensor(K, "K", shape, mem.dtype, self.device, contiguous=False)
-        vp = _tensor(V, "V", shape, mem.dtype, self.device, contiguous=False)
+        kp = _tensor(K, "K", shape, mem.dtype, self.device.index, contiguous=False)
+        vp = _tensor(V, "V", shape, mem.dtype, self.device.index, contiguous=False)
         ks, vs = K.stride(), V.stride()
         for st in (ks, vs):
             if st[3] != 1 or (st[2] != mem.head_dim and mem.n_kv_heads > 1):
                 raise ValueError("K, V: the heads of a token must be dense")
+        # (the stride of a dimension of one means nothing)
         _call(_lib.msa_cache8_append, self.device, stream, mem.handle, self._ref, kp, vp, T,
               ks[0] if self.batch > 1 else 0, ks[1] if T > 1 else 0,
               vs[0] if self.batch > 1 else 0, vs[1] if T > 1 else 0,
@@ -661,8 +685,8 @@ class Cache8:
             V_out = torch.empty(shape, dtype=mem.dtype, device=self.device)
         _call(_lib.msa_cache8_read, self.device, stream, mem.handle, self._ref,
               self._counts(begin, "begin"), rows,
-              _tensor(K_out, "K_out", shape, mem.dtype, self.device),
-              _tensor(V_out, "V_out", shape, mem.dtype, self.device))
+              _tensor(K_out, "K_out", shape, mem.dtype, self.device.index),
+              _tensor(V_out, "V_out", shape, mem.dtype, self.device.index))
         return K_out, V_out
 
     def attend_workspace_size(self, tokens: int, k: int, n_q_heads: int) -> int:
@@ -674,23 +698,23 @@ class Cache8:
         """Attention of the cache's newest tokens over the retrieved memory rows and the cached
         rows (msa_cache8_attend): Q, O [batch][tokens][n_q_heads][D], Q already rotated; lse
         [batch][tokens][n_q_heads] optional.  weight_decay None leaves ``weights`` alone."""
-        mem, dev = self.mem, self.device
-        if Q.dim() != 4:
+        mem, dev = self.mem, self.device.index
+        if not isinstance(Q, torch.Tensor) or Q.dim() != 4:
             raise ValueError("Q: expected [batch][tokens][n_q_heads][D]")
         T, H_q = Q.shape[1], Q.shape[2]
         shape = (self.batch, T, H_q, mem.head_dim)
         k = ids.shape[1] if ids is not None else 0
         if weight_decay is not None and not weight_decay >= 0.0:
             raise ValueError(f"weight_decay must be >= 0 or None, got {weight_decay}")
-        _call(_lib.msa_cache8_attend, dev, stream, mem.handle,
+        _call(_lib.msa_cache8_attend, self.device, stream, mem.handle,
               _tensor(content, "content", (mem.n_chunks, 2, mem.n_kv_heads, mem.head_dim), mem.dtype,
                       dev) if k else None,
               _tensor(ids, "ids", (self.batch, k), torch.int32, dev) if k else None, k, self._ref,
               T, H_q, _tensor(Q, "Q", shape, mem.dtype, dev), self._counts(n_tokens, "n_tokens"),
               _tensor(O, "O", shape, mem.dtype, dev),
               None if lse is None else _tensor(lse, "lse", shape[:3], torch.float32, dev),
-              -1.0 if weight_decay is None else weight_decay, workspace.data_ptr(),
-              workspace.numel() * workspace.element_size())
+              -1.0 if weight_decay is None else weight_decay,
+              *_buffer(workspace, "workspace", dev))
 
     def evict_workspace_size(self) -> int:
         return _lib.msa_cache8_evict_workspace_size(self.mem.handle, self._ref)
@@ -705,4 +729,4 @@ class Cache8:
                 self.mem.n_kv_heads, self.mem.head_dim):
             raise ValueError("out must be on the same device and have the same head shapes")
         _call(_lib.msa_cache8_evict, self.device, stream, self.mem.handle, self._ref, out._ref,
-              budget, recent, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+              budget, recent, *_buffer(workspace, "workspace", self.device.index))
