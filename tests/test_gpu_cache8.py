@@ -5,10 +5,10 @@ rounding is the same in any precision.  Attention bounds, per output, first orde
 u = 2^-23 (tensor-core sums may truncate):
   ds  = (D + 16) u A, A = max_j sum_d |q_d k_jd| / sqrt(D)          error of a score
   lse : ds + (rows + 8) u + 4 u |lse|
-  O   : (2 ds + 2^-11 + (rows + 16) u) sum_j p_j |v_j| + rows 2^-32 max|v|,
+  O   : (2 ds + 2^-11 + (rows + 16) u) sum_j p_j |v_j| + rows 2^-28 max|v|,
         2^-11 the rounding of a weight to fp16, the last term weights below fp16's normal
         range: half its smallest step, 2^-25, against weights kept at 2^11 2^(s - m) with m at
-        most 4 above the largest score, 2^-25 2^-11 2^4 = 2^-32 of the largest weight;
+        most 8 above the largest score, 2^-25 2^-11 2^8 = 2^-28 of the largest weight;
         a bf16 output adds half a step, 2^-8 |O|
   weights : (ds + lse's bound + 16 u) w a token."""
 import numpy as np
@@ -182,7 +182,7 @@ def run_attend(mem, content, cache, ref, ids, T, G, n, q_scale=1.0, decay=None, 
     nrow = cache.capacity + 4096
     ds = (D + 16) * U * amp
     tl = ds + (nrow + 8) * U + 4 * U * np.where(np.isfinite(wl), np.abs(wl), 0)
-    to = (2 * ds[..., None] + 2.0 ** -11 + (nrow + 16) * U) * pv + nrow * 2.0 ** -32 * vmax
+    to = (2 * ds[..., None] + 2.0 ** -11 + (nrow + 16) * U) * pv + nrow * 2.0 ** -28 * vmax
     if mem.dtype == torch.bfloat16:
         to = to + 2.0 ** -8 * (np.abs(want) + to)
     for b in range(B):

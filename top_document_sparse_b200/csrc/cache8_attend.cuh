@@ -21,9 +21,10 @@
 // int8 -> fp16 is a byte permute that sets the bits of 1024 + (q + 128) and
 // one subtraction.  Q is scaled by a power of two per column to 1 <= max|q| < 2, which loses
 // nothing of a bf16 row down to 2^-17 of its largest element.  P is kept at
-// 2^11 times its size against a reference that moves, to 4 above the score (log2
+// 2^11 times its size against a reference that moves, to 8 above the score (log2
 // units), only when a score exceeds it by 4: at most 2^15, and weights down to
-// 2^-21 of the largest keep fp16's full 11 bits.
+// 2^-17 of the largest keep fp16's full 11 bits, smaller ones an error below
+// 2^-28 of the largest.
 //   Memory rows are bf16 and go through bf16 MMAs; P is split there into a bf16
 // head and tail, two MMAs, so it loses nothing either.
 #pragma once
@@ -40,7 +41,7 @@ constexpr int kC8Warps = 4;
 constexpr int kC8Stages = 3;          // tiles of a warp in flight or in use
 constexpr float kC8Shift = 11.0f;     // P is 2^11 exp2(s - m)
 constexpr float kC8Slack = 4.0f;      // a score may exceed m by this before m moves,
-constexpr float kC8Lead = 4.0f;       // and m then moves this far above it
+constexpr float kC8Lead = 8.0f;       // and m then moves this far above it
 constexpr float kC8MinUnit = 0x1p-60f;  // smallest unit of O
 
 struct Attend8Args {

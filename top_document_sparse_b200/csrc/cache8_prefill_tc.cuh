@@ -231,8 +231,9 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
   const int nblk = u1 - u0;
   const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
 
-  // bounded wait; false (and every later wait false at once) after a timeout anywhere
+  // bounded wait; false (and every later wait that would block, at once) after a timeout anywhere
   auto wait = [&](int i, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar(i), parity)) return true;
     if (*fail) return false;
     if (mbar_wait(bar(i), parity)) return true;
     *fail = 1;
@@ -252,6 +253,10 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       if (j >= kC8tSlots)
         live = live && wait((h ? kCbFreeV0 : kCbFreeK0) + j % kC8tSlots, (j / kC8tSlots - 1) & 1);
       return live;
+    };
+    // both scales of a block go out with K, so that S's barrier brings them to the softmax
+    auto put_scales = [&](int j, float k, float v) {
+      *reinterpret_cast<float2 *>(scales + 2 * (j % (2 * kC8tSlots))) = make_float2(k, v);
     };
     auto landed = [&](int j, int h) {
       fence_proxy_async_smem();  // the rows become visible to the tensor cores
@@ -281,15 +286,21 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     load_raw(u0, 1);
     const int nl = max(0, min(u1, lb) - u0);  // local blocks of this split
     for (int j = 0; j < nl; ++j) {
+      float mx[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float mx = 0.0f;
+        if (h == 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) mx = fmaxf(mx, rs[h][i]);
-        if (mx == 0.0f) mx = 1.0f;  // rows of zeros
-        const float inv = 1.0f / mx;  // a power of two
+          for (int e = 0; e < 2; ++e) {
+            mx[e] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) mx[e] = fmaxf(mx[e], rs[e][i]);
+            if (mx[e] == 0.0f) mx[e] = 1.0f;  // rows of zeros
+          }
+        }
+        const float inv = 1.0f / mx[h];  // a power of two
         if (!wait_slot(j, h)) continue;
-        if (tid == 0) scales[2 * (j % (2 * kC8tSlots)) + h] = mx;
+        if (h == 0 && tid == 0) put_scales(j, mx[0], mx[1]);
         uint8_t *dst = slot(j, h);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -307,38 +318,47 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         landed(j, h);
       }
     }
-    // memory rows, bf16: pieces of 8 elements, 16 a row
+    // memory rows, bf16: pieces of 8 elements, 16 a row; V's largest element is found before K goes
+    // out, V being read a second time for its conversion
     const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
+    constexpr int M = kC8tBlk / 8;
     for (int j = nl; j < nblk; ++j) {
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
+      uint4 w[M];
+      float mx[2];
+      auto load = [&](int h) {
         const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.content) + h * kv + g * D + 8 * (tid & 15);
         const int x0 = (u0 + j - lb) * kC8tBlk + (tid >> 4);
-        constexpr int M = kC8tBlk / 8;
-        uint4 w[M];
-        float mx = 0.0f;
 #pragma unroll
         for (int i = 0; i < M; ++i) {
           const int x = x0 + 8 * i;
           w[i] = make_uint4(0, 0, 0, 0);
           if (x < n_mem) w[i] = *reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(table[x]) * 2 * kv);
         }
+      };
+#pragma unroll 1
+      for (int h = 1; h >= 0; --h) {
+        load(h);
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < M; ++i) {
           const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            mx = max3(mx, finite_abs(__uint_as_float(y[e] << 16)), finite_abs(__uint_as_float(y[e] & 0xffff0000u)));
+            top = max3(top, finite_abs(__uint_as_float(y[e] << 16)), finite_abs(__uint_as_float(y[e] & 0xffff0000u)));
         }
-        mx = warp_max(mx);
+        top = warp_max(top);
         asm volatile("bar.sync 1, %0;" ::"n"(kC8tConv) : "memory");  // `red` was read
-        if (lane == 0) red[warp - 10] = mx;
+        if (lane == 0) red[warp - 10] = top;
         asm volatile("bar.sync 1, %0;" ::"n"(kC8tConv) : "memory");
-        mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        mx = mx > 0.0f ? floor_pow2(mx) : 1.0f;
+        top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        mx[h] = top > 0.0f ? floor_pow2(top) : 1.0f;
+      }
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {  // w holds K
+        if (h == 1) load(1);
         if (!wait_slot(j, h)) continue;
-        if (tid == 0) scales[2 * (j % (2 * kC8tSlots)) + h] = mx;
-        const float inv = 1.0f / mx;
+        if (h == 0 && tid == 0) put_scales(j, mx[0], mx[1]);
+        const float inv = 1.0f / mx[h];
 #pragma unroll
         for (int i = 0; i < M; ++i) {
           const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -453,14 +473,13 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     bool okw = true;
     for (int j = 0; j < nblk; ++j) {
       const int u = u0 + j;
-      // V's barrier brings both scales
-      okw = __all_sync(0xffffffffu, wait(kCbFullV0 + j % kC8tSlots, (j / kC8tSlots) & 1) &&
-                                        wait(kCbS0 + 2 * x + (j & 1), (j >> 1) & 1));
+      okw = __all_sync(0xffffffffu, wait(kCbS0 + 2 * x + (j & 1), (j >> 1) & 1));
       if (!okw) break;
       tc05_fence_after();
       // (positive even where the product underflows, so that a hidden row stays at -inf)
-      float c = fmaxf(cf * scales[2 * (j % (2 * kC8tSlots))], 1.2e-38f);
-      const float v_scale = scales[2 * (j % (2 * kC8tSlots)) + 1];
+      const float2 kv_scale = *reinterpret_cast<const float2 *>(scales + 2 * (j % (2 * kC8tSlots)));
+      float c = fmaxf(cf * kv_scale.x, 1.2e-38f);
+      const float v_scale = kv_scale.y;
       const float unit_new = fmaxf(unit, v_scale);
       // whole power of two: V's scale over the unit
       const int lr = (__float_as_int(v_scale) >> 23) - (__float_as_int(unit_new) >> 23);

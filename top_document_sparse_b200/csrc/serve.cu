@@ -359,11 +359,11 @@ msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B
       auto wk = msa::cache8_weight_kernel<D, NT, FMT>;
       const int ws = msa::Weight8Smem<D, NT>::kBytes;
       MSA_CUDA(allow_smem(wk, ws));
-      // one round of columns: a CTA streams its share of the tiles, about five CTAs an SM in all
+      // one round of columns: a CTA streams its share of the tiles, about eight CTAs an SM in all
       // (a CTA's set-up takes as long as a dozen tiles); more rounds: a CTA for every kC8wRows rows
       const int chunks = (a.cap + msa::kC8wRows - 1) / msa::kC8wRows;
       const bool stream = static_cast<int64_t>(a.T) * a.G <= 8 * NT;
-      const int grid_x = stream ? std::min(chunks, (5 * num_sms() + B * a.H_kv - 1) / (B * a.H_kv)) : chunks;
+      const int grid_x = stream ? std::min(chunks, (8 * num_sms() + B * a.H_kv - 1) / (B * a.H_kv)) : chunks;
       MSA_CUDA(launch_pdl(wk, dim3(grid_x, B * a.H_kv), block, ws, st, a, stream ? 1 : 0));
     } else
       MSA_CUDA(launch_pdl(msa::cache8_weight_f32_kernel<D, FMT>,
