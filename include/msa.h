@@ -513,7 +513,8 @@ MSA_API msa_status msa_sparse_attend_backward(const msa_memory *mem, const void 
  * head_dim 2..512 and rotary_dim 2..head_dim, both even (NTK: rotary_dim > 2).
  * Frequencies are kept as 64-bit fractions of a turn, so an angle is exact
  * modulo one turn at every int64 position (negative ones too).  The handle is
- * immutable and belongs to the device that was current at its creation.
+ * immutable and belongs to the device that was current at its creation, where
+ * its calls have to be made; the same holds for a memory in the msa_cache8_* calls.
  */
 typedef enum { MSA_ROPE_HALF = 0, MSA_ROPE_INTERLEAVED = 1 } msa_rope_layout;
 typedef enum {
@@ -649,7 +650,10 @@ MSA_API size_t msa_cache8_attend_workspace_size(const msa_memory *mem, const msa
  *              the heads of kv head g (0 overwrites; rows beyond cache_len stay)
  * k may be 0 (content and ids are then not read).  A group
  * (n_q_heads / H_kv) is at most 16.  A count out of [0, tokens] or a length
- * outside [0, capacity] counts as no tokens (MSA_DEVERR_BAD_LENGTH).
+ * outside [0, capacity] counts as no tokens (MSA_DEVERR_BAD_LENGTH).  O must
+ * not overlap Q.  As with every call here that takes a workspace, calls that
+ * may run at the same time need one each; nothing in it has to survive or to
+ * be cleared between calls, so ordered calls and graphs may share one.
  */
 MSA_API msa_status msa_cache8_attend(const msa_memory *mem, const void *content,
                                      const int32_t *ids, int32_t k, const msa_cache8 *cache,
@@ -657,6 +661,16 @@ MSA_API msa_status msa_cache8_attend(const msa_memory *mem, const void *content,
                                      const int32_t *n_tokens, void *O, float *lse,
                                      float weight_decay, void *workspace,
                                      size_t workspace_bytes, msa_stream stream);
+
+/* msa_cache8_attend over the memory rows the last msa_fetch of `f` placed in
+ * its slot cache (same ids, batch and k). */
+MSA_API msa_status msa_cache8_attend_fetched(const msa_memory *mem, const msa_fetcher *f,
+                                             const int32_t *ids, int32_t k,
+                                             const msa_cache8 *cache, int32_t tokens,
+                                             int32_t n_q_heads, const void *Q,
+                                             const int32_t *n_tokens, void *O, float *lse,
+                                             float weight_decay, void *workspace,
+                                             size_t workspace_bytes, msa_stream stream);
 
 /* Scratch bytes msa_cache8_evict needs. */
 MSA_API size_t msa_cache8_evict_workspace_size(const msa_memory *mem, const msa_cache8 *cache);
@@ -676,6 +690,8 @@ MSA_API size_t msa_cache8_evict_workspace_size(const msa_memory *mem, const msa_
  *         budget); it needs weights too.  Its weights of rows that the query
  *         no longer holds become 0; its other bytes there stay.
  *   budget >= block_len; 0 <= recent <= budget
+ * A length outside [0, capacity] is flagged (MSA_DEVERR_BAD_LENGTH) and taken
+ * as the nearer bound.
  */
 MSA_API msa_status msa_cache8_evict(const msa_memory *mem, const msa_cache8 *cache,
                                     const msa_cache8 *out, int32_t budget, int32_t recent,

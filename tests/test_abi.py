@@ -136,3 +136,8 @@ def test_serving_calls_reject_null_handles():
                                  0, None) == 1
     assert lib.msa_cache8_evict_workspace_size(None, None) == 0
     assert lib.msa_cache8_evict(None, None, None, 64, 0, None, 0, None) == 1
+
+
+def test_attend_fetched_rejects_null_handles():
+    assert msa.lib().msa_cache8_attend_fetched(None, None, None, 0, None, 1, 1, None, None, None, None,
+                                               -1.0, None, 0, None) == 1

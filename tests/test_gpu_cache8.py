@@ -220,6 +220,13 @@ ATT = [
     ("bf16", "e4m3", 128, 2, 3, 41, 320, 64, [41, 320, 133], [41, 7, 0], 4),
     ("bf16", "int8", 128, 1, 8, 70, 192, 64, [192, 71], [70, 70], 5),
     ("bf16", "int8", 64, 2, 2, 150, 448, 64, [448, 150, 149], None, 2),
+    # tensor cores (48 columns of a kv head and more, D = 128): several splits and ring rounds, odd
+    # groups, one and two tiles, queries that see nothing, every block length
+    ("bf16", "int8", 128, 2, 4, 33, 1024, 16, [1024, 700], [33, 20], 6),
+    ("bf16", "e4m3", 128, 1, 16, 20, 2048, 128, [2048], None, 0),
+    ("bf16", "int8", 128, 1, 3, 16, 192, 64, [5, 16, 0], [16, 9, 0], 0),
+    ("bf16", "e4m3", 128, 1, 5, 29, 1088, 32, [1087, 29, 64], None, 3),
+    ("bf16", "int8", 128, 1, 1, 48, 64, 32, [48, 64], [47, 48], 1),
     ("f32", "int8", 64, 2, 2, 1, 256, 64, [1, 31, 33, 256], None, 3),
     ("f32", "e4m3", 128, 1, 5, 9, 128, 16, [9, 128, 4, 0], [9, 3, 9, 0], 2),
     ("f32", "e4m3", 64, 1, 1, 3, 64, 32, [2, 0], [3, 0], 0),
@@ -239,9 +246,11 @@ def test_attend_matches_fp64(case):
 
 
 @pytest.mark.parametrize("dt,fmt,T,G,decay", [("bf16", "int8", 1, 4, 0.0), ("bf16", "e4m3", 7, 3, 1.0),
-                                              ("f32", "int8", 2, 2, 0.5), ("bf16", "int8", 40, 2, 0.9)])
+                                              ("f32", "int8", 2, 2, 0.5), ("bf16", "int8", 40, 2, 0.9),
+                                              ("bf16", "e4m3", 30, 3, 0.25)])
 def test_attend_accumulates_weights(dt, fmt, T, G, decay):
-    mem, content = memory(torch.bfloat16 if dt == "bf16" else torch.float32, 2, 64)
+    D = 128 if T == 30 else 64
+    mem, content = memory(torch.bfloat16 if dt == "bf16" else torch.float32, 2, D)
     lens, n = [200, 1, 77, 150], [T, 1, T // 2, T]
     cache, ref = filled(mem, 4, 256, 32, fmt, lens, seed=9, track=True)
     ids = torch.tensor([[0, 3], [1, 2], [5, 4], [3, 0]], dtype=torch.int32, device="cuda")
@@ -257,6 +266,125 @@ def test_attend_magnitudes(q_scale, spread):
     ids = torch.tensor([[0, 3], [1, 5]], dtype=torch.int32, device="cuda")
     run_attend(mem, content, cache, ref, ids, 1, 4, None, q_scale=q_scale)
     run_attend(mem, content, cache, ref, None, 6, 2, None, q_scale=q_scale)
+    run_attend(mem, content, cache, ref, ids, 40, 2, None, q_scale=q_scale)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("k_scale,v_scale", [(2.0 ** -30, 2.0 ** 40), (8.0, 2.0 ** -40), (0.0, 0.0)])
+def test_attend_memory_magnitudes(T, k_scale, v_scale):
+    """Memory rows far larger and far smaller than the cached ones, and all-zero ones."""
+    mem, content = memory(torch.bfloat16, 1, 128)
+    content[:, 0] *= k_scale
+    content[:, 1] *= v_scale
+    cache, ref = filled(mem, 2, 256, 64, "int8", [256, 50], seed=6)
+    ids = torch.tensor([[0, 3, 5], [1, 5, 2]], dtype=torch.int32, device="cuda")
+    run_attend(mem, content, cache, ref, ids, T, 2, None)
+
+
+def test_attend_over_fetched_rows_equals_resident_rows():
+    """The host tier's slot cache holds the same rows elsewhere: the same bits."""
+    from top_document_sparse_b200 import msa
+    mem, content = memory(torch.bfloat16, 2, 128)
+    host = mem.new_content(device="cpu", pin_memory=True)
+    host.copy_(content)
+    fetcher = msa.Fetcher(mem, host, n_slots=9, max_batch=2, max_k=3)
+    ids = torch.tensor([[0, 3, 5], [1, 5, 2]], dtype=torch.int32, device="cuda")
+    for T, G in ((1, 4), (17, 3)):
+        cache, ref = filled(mem, 2, 256, 64, "e4m3", [256, 50], seed=6)
+        O, lse = run_attend(mem, content, cache, ref, ids, T, G, None)
+        fetcher.fetch(ids)
+        Q = torch.randn(2, T, 2 * G, 128, generator=torch.Generator(device="cuda").manual_seed(11),
+                        device="cuda").bfloat16()
+        O2, lse2 = torch.empty_like(O), torch.empty_like(lse)
+        cache.attend(fetcher, ids, Q, O2, msa.workspace(cache.attend_workspace_size(T, 3, 2 * G)), lse=lse2)
+        assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    other, _ = memory(torch.bfloat16, 2, 128)
+    with pytest.raises(msa.MsaError):
+        c = msa.Cache8(other, 2, 64)
+        c.attend(fetcher, ids, Q, O2, msa.workspace(c.attend_workspace_size(T, 3, 2 * G)))
+
+
+def test_attend_and_append_past_32_bit_offsets():
+    """A cache of 2^31 elements and more: the last query's rows lie past every 32-bit offset.  Checked
+    on one head against torch in fp64."""
+    from top_document_sparse_b200 import msa
+    B, H, cap, D = 2, 8, (1 << 20) + 128, 128
+    mem, content = memory(torch.bfloat16, H, D)
+    cache = msa.Cache8(mem, B, cap, 128, "int8", track_weights=True)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for t in (cache.k, cache.v):
+        for b in range(B):
+            t[b] = torch.randint(-100, 101, (H, cap, D), generator=g, device="cuda", dtype=torch.int8)
+    cache.k_scale.fill_(2.0 ** -6)
+    cache.v_scale.fill_(2.0 ** -6)
+    start = torch.tensor([5, cap - 3], dtype=torch.int32, device="cuda")
+    kv = torch.randn(2, B, 2, H, D, generator=g, device="cuda").bfloat16()
+    cache.append(kv[0], kv[1], start=start)
+    Kr, _ = cache.read(start, 2)
+    assert torch.all((Kr.float() - kv[0].float()).abs() <= 2.0 ** -6)  # half a step of the largest scale
+    for T, G in ((1, 1), (2, 24 // 2)):
+        Q = torch.randn(B, T, H * G, D, generator=g, device="cuda").bfloat16()
+        O, lse = torch.empty_like(Q), torch.empty(B, T, H * G, device="cuda")
+        cache.attend(None, None, Q, O, msa.workspace(cache.attend_workspace_size(T, 0, H * G)), lse=lse,
+                     weight_decay=0.0)
+        b, h, n = 1, H - 1, cap - 1
+        sk = cache.k_scale[b, h].double().repeat_interleave(128)[:n, None]
+        sv = cache.v_scale[b, h].double().repeat_interleave(128)[:n, None]
+        V = cache.v[b, h, :n].double() * sv
+        z = (cache.k[b, h, :n].double() * sk) @ Q[b, -1, h * G].double() / D ** 0.5
+        p = torch.softmax(z, 0)
+        want, size = p @ V, p @ V.abs()
+        # see the bounds above; the row sum's error grows with the square root of the rows here, but
+        # is bounded by (rows / 512) u: a split's lane adds that many terms
+        tol = (2.0 ** -11 + 2.0 ** -12 + n / 512 * U) * size + n * 2.0 ** -28 * 2
+        err = (O[b, -1, h * G].double() - want).abs()
+        assert torch.all(err <= tol + 2.0 ** -8 * (want.abs() + tol))
+        assert abs(float(lse[b, -1, h * G]) - float(torch.logsumexp(z, 0))) <= 1e-4
+        assert abs(float(cache.weights[b, h, :n].sum()) - T * G) <= 1e-3 * T * G
+    assert msa.device_error() == 0
+
+
+def test_attend_calls_on_two_streams_and_two_graphs_of_one_workspace():
+    from top_document_sparse_b200 import msa
+    mem, content = memory(torch.bfloat16, 2, 128)
+    ids = torch.tensor([[0, 3], [1, 5]], dtype=torch.int32, device="cuda")
+    sets = []
+    for seed, T in ((1, 1), (2, 3), (3, 40)):
+        cache, _ = filled(mem, 2, 1024, 64, "int8", [1024, 777], seed=seed, track=True)
+        Q = torch.randn(2, T, 6, 128, device="cuda").bfloat16()
+        need = cache.attend_workspace_size(T, 2, 6)
+        sets.append((cache, Q, torch.empty_like(Q), need))
+    want = []
+    for cache, Q, O, need in sets:
+        cache.attend(content, ids, Q, O, msa.workspace(need), weight_decay=0.0)
+        want.append((O.clone(), cache.weights.clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    spaces = [msa.workspace(need) for *_, need in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):  # at the same time, a workspace each
+        for (cache, Q, O, _), st, ws in zip(sets, streams, spaces):
+            cache.attend(content, ids, Q, O, ws, weight_decay=0.0, stream=st)
+    torch.cuda.synchronize()
+    for (cache, _, O, _), (o, w) in zip(sets, want):
+        # (as bits: the weights behind the last row hold the poison, NaN)
+        assert torch.equal(O, o) and torch.equal(cache.weights.view(torch.int32), w.view(torch.int32))
+    shared = msa.workspace(max(need for *_, need in sets))
+    graphs = []
+    for cache, Q, O, _ in sets:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            cache.attend(content, ids, Q, O, shared, weight_decay=0.0)
+        graphs.append(gr)
+    for order in ((0, 1, 2), (2, 0, 1), (1, 2, 0)):
+        for i in order:
+            sets[i][2].zero_()
+            graphs[i].replay()
+    torch.cuda.synchronize()
+    for (cache, _, O, _), (o, w) in zip(sets, want):
+        # (as bits: the weights behind the last row hold the poison, NaN)
+        assert torch.equal(O, o) and torch.equal(cache.weights.view(torch.int32), w.view(torch.int32))
+    assert msa.device_error() == 0
 
 
 def test_attend_flags_bad_counts():
@@ -280,6 +408,7 @@ EVICT = [
     ("e4m3", 64, 3, 16, 2048, [2047, 17, 2048, 1031], 16, 0),
     ("int8", 64, 1, 32, 256, [255, 256, 129, 128, 97], 128, 128),
     ("e4m3", 128, 1, 128, 512, [512, 500, 129, 256], 129, 1),
+    ("int8", 64, 1, 16, 16 * 10304, [16 * 10304 - 3], 16 * 9000 + 5, 100),  # keys in the workspace
 ]
 
 
@@ -420,3 +549,34 @@ def test_refusals():
         with pytest.raises((ValueError, TypeError, msa.MsaError)):
             bad()
     assert msa.launch_count() == before, "a refused call enqueued something"
+
+
+def test_evict_flags_bad_lengths():
+    from top_document_sparse_b200 import msa
+    mem, _ = memory(torch.bfloat16, 1, 64)
+    cache, _ = filled(mem, 3, 128, 16, "int8", [128, 100, 10], seed=1, track=True)
+    cache.weights.zero_()
+    cache.cache_len.copy_(torch.tensor([129, -1, 10]))
+    cache.evict(64, 0, msa.workspace(cache.evict_workspace_size()))
+    assert msa.device_error() == msa.DEVERR_BAD_LENGTH
+    assert cache.cache_len.tolist() == [64, 0, 10]
+
+
+def test_append_of_many_shapes_at_once_equals_block_by_block():
+    """Units that share a CTA (small blocks), one of them with non-finite values, against the same
+    rows appended to caches of one head."""
+    from top_document_sparse_b200 import msa
+    for D, bl, H in ((64, 16, 3), (128, 16, 5), (64, 32, 1)):
+        mem, _ = memory(torch.bfloat16, H, D)
+        one, _ = memory(torch.bfloat16, 1, D)
+        kv = torch.randn(2, 2, 50, H, D, device="cuda").bfloat16()
+        kv[0, 1, 20, H - 1, 3] = float("inf")
+        kv[1, 0, 33, 0, 5] = float("nan")
+        cache = msa.Cache8(mem, 2, 64, bl, "int8")
+        cache.append(kv[0], kv[1])
+        for h in range(H):
+            single = msa.Cache8(one, 2, 64, bl, "int8")
+            single.append(kv[0][:, :, h:h + 1].contiguous(), kv[1][:, :, h:h + 1].contiguous())
+            assert torch.equal(cache.k[:, h:h + 1], single.k) and torch.equal(cache.v[:, h:h + 1], single.v)
+            assert torch.equal(cache.k_scale[:, h:h + 1], single.k_scale)
+            assert torch.equal(cache.v_scale[:, h:h + 1], single.v_scale)

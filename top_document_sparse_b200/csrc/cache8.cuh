@@ -411,6 +411,7 @@ cache8_select_kernel(const float *__restrict__ weights, const int32_t *__restric
   if (blockIdx.x % H_kv == 0 && threadIdx.x == 0) {
     lens[2 * b] = p.len;
     lens[2 * b + 1] = p.new_len;
+    if (p.len != cache_len[b]) raise_device_error(MSA_DEVERR_BAD_LENGTH);
   }
   int32_t *src = src_block + bh * (nb + 1);
   uint32_t *key = smem_keys ? key_sm : keys + bh * nb;

@@ -48,6 +48,8 @@ struct Attend8Args {
   const void *content;
   const int32_t *ids;
   const int64_t *doc_chunk_off;
+  const int32_t *slots;  // a host tier's slot cache: slot of each (query, rank), or null
+  int slot_chunks;
   int k, n_docs, table_cap;
   const uint8_t *k8, *v8;
   const float *ks, *vs;
@@ -448,7 +450,7 @@ cache8_attend_kernel(Attend8Args a) {
   int n_mem = 0;
   if (a.k > 0 && (!own_mem || split >= a.loc_split))
     n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
-                              nullptr, 0, table, pre, base, a.table_cap);
+                              a.slots ? a.slots + static_cast<int64_t>(b) * a.k : nullptr, a.slot_chunks, table, pre, base, a.table_cap);
   __syncthreads();
 
   const __half *qh = reinterpret_cast<const __half *>(sm + Sm::kQ);
@@ -708,7 +710,7 @@ cache8_attend_f32_kernel(Attend8Args a) {
   int n_mem = 0;
   if (a.k > 0)
     n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
-                              nullptr, 0, table, pre, base, a.table_cap);
+                              a.slots ? a.slots + static_cast<int64_t>(b) * a.k : nullptr, a.slot_chunks, table, pre, base, a.table_cap);
   __syncthreads();
   const int last_col = min(c0 + C, q.n * a.G) - 1;
   const int n_loc = max(0, column_rows(a, q, last_col));

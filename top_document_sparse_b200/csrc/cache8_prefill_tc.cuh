@@ -218,7 +218,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
   int n_mem = 0;
   if (a.k > 0)
     n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
-                              nullptr, 0, table, pre, base, a.table_cap);
+                              a.slots ? a.slots + static_cast<int64_t>(b) * a.k : nullptr, a.slot_chunks, table, pre, base, a.table_cap);
   tc05_fence_before();
   __syncthreads();  // barriers, the fail flag and the TMEM address are visible
   tc05_fence_after();

@@ -174,4 +174,12 @@ inline size_t elem_size(msa_dtype t) { return t == MSA_BF16 ? 2 : 4; }
 // a word of its own): enqueue a read into *bits and a clear on `st`.
 cudaError_t take_serve_error(unsigned int *bits, cudaStream_t st);
 
+// The 8-bit cache's attention over memory rows in `content`, or in a slot cache (slots, [batch][k],
+// of slot_chunks rows each); see msa_cache8_attend.
+msa_status cache8_attend(const msa_memory *mem, const void *content, const int32_t *ids,
+                         const int32_t *slots, int slot_chunks, int32_t k, const msa_cache8 *cache,
+                         int32_t tokens, int32_t n_q_heads, const void *Q, const int32_t *n_tokens,
+                         void *O, float *lse, float weight_decay, void *workspace,
+                         size_t workspace_bytes, cudaStream_t st);
+
 }  // namespace msa_host

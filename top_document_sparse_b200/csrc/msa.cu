@@ -459,7 +459,7 @@ msa_status attend_impl(const msa_memory *mem, const void *content, const int32_t
 // ===================================================================== C ABI
 extern "C" {
 
-int32_t msa_version(void) { return 1 * 10000 + 0 * 100 + 0; }
+int32_t msa_version(void) { return 1 * 10000 + 1 * 100 + 0; }
 
 uint64_t msa_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
@@ -887,6 +887,21 @@ msa_status msa_sparse_attend_fetched(const msa_memory *mem, const msa_fetcher *f
                      n_q_heads, Q, K_new, V_new, K_cache, V_cache, cache_len, cache_capacity,
                      pos_offset, O, workspace, workspace_bytes,
                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_cache8_attend_fetched(const msa_memory *mem, const msa_fetcher *f,
+                                     const int32_t *ids, int32_t k, const msa_cache8 *cache,
+                                     int32_t tokens, int32_t n_q_heads, const void *Q,
+                                     const int32_t *n_tokens, void *O, float *lse,
+                                     float weight_decay, void *workspace, size_t workspace_bytes,
+                                     msa_stream stream) {
+  if (!mem || !f || !cache) return fail(MSA_ERR_INVALID_ARG, "null memory, fetcher or cache");
+  if (f->mem != mem) return fail(MSA_ERR_INVALID_ARG, "fetcher belongs to another memory");
+  if (cache->batch > f->max_batch || k > f->max_k)
+    return fail(MSA_ERR_INVALID_ARG, "batch / k beyond the fetcher's sizes");
+  return cache8_attend(mem, f->slot_cache, ids, f->d_slots, mem->max_doc_chunks, k, cache, tokens,
+                       n_q_heads, Q, n_tokens, O, lse, weight_decay, workspace, workspace_bytes,
+                       reinterpret_cast<cudaStream_t>(stream));
 }
 
 msa_status msa_step_host(const msa_memory *mem, const void *router_keys, msa_fetcher *f,

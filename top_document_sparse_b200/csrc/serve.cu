@@ -68,6 +68,15 @@ cudaError_t allow_smem(K kern, int bytes) {
   return cudaSuccess;
 }
 
+// The tables of a handle are on the device that was current at its creation.
+msa_status current_device(int device, const char *what) {
+  int dev = 0;
+  MSA_CUDA(cudaGetDevice(&dev));
+  if (dev != device)
+    return fail(MSA_ERR_INVALID_ARG, "the %s is on device %d, the current device is %d", what, device, dev);
+  return MSA_OK;
+}
+
 // ---------------------------------------------------------------- rotary positions
 msa_status rope_frequencies(const msa_rope_config *c, std::vector<uint64_t> &freq, float *magnitude) {
   const int r = c->rotary_dim;
@@ -161,6 +170,8 @@ msa_status cache8_check(const msa_memory *mem, const msa_cache8 *c) {
                 (long long)c->batch * mem->H_kv);
   if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->cache_len)
     return fail(MSA_ERR_INVALID_ARG, "null cache buffer");
+  const msa_status on = current_device(mem->device, "memory");
+  if (on != MSA_OK) return on;
   if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
       !aligned16(c->weights))
     return fail(MSA_ERR_INVALID_ARG, "cache buffers must be 16-byte aligned");
@@ -387,6 +398,70 @@ EvictPlan8 plan_evict8(const msa_memory *mem, const msa_cache8 *c) {
 
 }  // namespace
 
+msa_status msa_host::cache8_attend(const msa_memory *mem, const void *content, const int32_t *ids,
+                                   const int32_t *slots, int slot_chunks, int32_t k,
+                                   const msa_cache8 *cache, int32_t tokens, int32_t n_q_heads,
+                                   const void *Q, const int32_t *n_tokens, void *O, float *lse,
+                                   float weight_decay, void *workspace, size_t workspace_bytes,
+                                   cudaStream_t st) {
+  const msa_status s = attend8_check(mem, cache, tokens, k, n_q_heads);
+  if (s != MSA_OK) return s;
+  if (!Q || !O || (k > 0 && (!content || !ids))) return fail(MSA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(Q) || !aligned16(O) || !aligned16(content) || !aligned16(workspace))
+    return fail(MSA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (std::isnan(weight_decay) || std::isinf(weight_decay))
+    return fail(MSA_ERR_INVALID_ARG, "weight_decay must be finite");
+  const bool track = weight_decay >= 0.0f;
+  if (track && !cache->weights)
+    return fail(MSA_ERR_INVALID_ARG, "weight_decay >= 0 needs a cache with weights");
+  const Attend8Plan p = plan_attend8(mem, cache, tokens, k, n_q_heads);
+  if (workspace_bytes < p.bytes || (p.bytes > 0 && !workspace))
+    return fail(MSA_ERR_INVALID_ARG, "workspace too small: %zu < %zu", workspace_bytes, p.bytes);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  msa::Attend8Args a;
+  a.content = content;
+  a.ids = ids;
+  a.doc_chunk_off = mem->d_doc_chunk_off;
+  a.slots = slots;
+  a.slot_chunks = slot_chunks;
+  a.k = k;
+  a.n_docs = mem->n_docs;
+  a.table_cap = p.table_cap;
+  a.k8 = static_cast<const uint8_t *>(cache->k);
+  a.v8 = static_cast<const uint8_t *>(cache->v);
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.cache_len = cache->cache_len;
+  a.n_tokens = n_tokens;
+  a.H_kv = mem->H_kv;
+  a.G = n_q_heads / mem->H_kv;
+  a.g_magic = a.G == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + a.G - 1) / a.G);
+  a.T = tokens;
+  a.cap = cache->capacity;
+  a.bl = cache->block_len;
+  a.bl_shift = cache->block_len == 16 ? 4 : cache->block_len == 32 ? 5 : cache->block_len == 64 ? 6 : 7;
+  a.Q = Q;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(mem->D)));
+  a.n_split = p.n_split;
+  a.loc_split = p.loc_split;
+  a.O = O;
+  a.lse = lse ? lse : track ? reinterpret_cast<float *>(ws + p.lse) : nullptr;
+  a.part_o = reinterpret_cast<float *>(ws + p.part_o);
+  a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
+  a.weights = track ? cache->weights : nullptr;
+  a.decay = weight_decay;
+  const int nt = attend8_nt(static_cast<int>(std::min<int64_t>(static_cast<int64_t>(tokens) * a.G, 64)));
+  return dispatch8(mem, cache->format, [&](auto t, auto d, auto f) {
+    using T = decltype(t);
+    if (sizeof(T) == 4 || nt == 1) return launch_attend8<T, d.value, f.value, 1>(a, p, cache->batch, st);
+    if constexpr (sizeof(T) == 2) {
+      if (nt == 2) return launch_attend8<T, d.value, f.value, 2>(a, p, cache->batch, st);
+      return launch_attend8<T, d.value, f.value, 4>(a, p, cache->batch, st);
+    }
+    return MSA_OK;
+  });
+}
+
 // ===================================================================== C ABI
 extern "C" {
 
@@ -473,6 +548,8 @@ msa_status msa_rope_apply(const msa_rope *rope, msa_dtype dtype, int64_t tokens,
     if (s->in == s->out && s->in_stride != s->out_stride)
       return fail(MSA_ERR_INVALID_ARG, "in place, the strides must be equal");
   }
+  const msa_status on = current_device(rope->device, "rotary handle");
+  if (on != MSA_OK) return on;
   const int inv = inverse ? 1 : 0;
   return dtype == MSA_BF16
              ? dispatch_rope<__nv_bfloat16>(rope, tokens, positions, inv, qs, ks, to_stream(stream))
@@ -542,61 +619,8 @@ msa_status msa_cache8_attend(const msa_memory *mem, const void *content, const i
                              const void *Q, const int32_t *n_tokens, void *O, float *lse,
                              float weight_decay, void *workspace, size_t workspace_bytes,
                              msa_stream stream) {
-  const msa_status s = attend8_check(mem, cache, tokens, k, n_q_heads);
-  if (s != MSA_OK) return s;
-  if (!Q || !O || (k > 0 && (!content || !ids))) return fail(MSA_ERR_INVALID_ARG, "null pointer argument");
-  if (!aligned16(Q) || !aligned16(O) || !aligned16(content) || !aligned16(workspace))
-    return fail(MSA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
-  if (std::isnan(weight_decay) || std::isinf(weight_decay))
-    return fail(MSA_ERR_INVALID_ARG, "weight_decay must be finite");
-  const bool track = weight_decay >= 0.0f;
-  if (track && !cache->weights)
-    return fail(MSA_ERR_INVALID_ARG, "weight_decay >= 0 needs a cache with weights");
-  const Attend8Plan p = plan_attend8(mem, cache, tokens, k, n_q_heads);
-  if (workspace_bytes < p.bytes || (p.bytes > 0 && !workspace))
-    return fail(MSA_ERR_INVALID_ARG, "workspace too small: %zu < %zu", workspace_bytes, p.bytes);
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  msa::Attend8Args a;
-  a.content = content;
-  a.ids = ids;
-  a.doc_chunk_off = mem->d_doc_chunk_off;
-  a.k = k;
-  a.n_docs = mem->n_docs;
-  a.table_cap = p.table_cap;
-  a.k8 = static_cast<const uint8_t *>(cache->k);
-  a.v8 = static_cast<const uint8_t *>(cache->v);
-  a.ks = cache->k_scale;
-  a.vs = cache->v_scale;
-  a.cache_len = cache->cache_len;
-  a.n_tokens = n_tokens;
-  a.H_kv = mem->H_kv;
-  a.G = n_q_heads / mem->H_kv;
-  a.g_magic = a.G == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + a.G - 1) / a.G);
-  a.T = tokens;
-  a.cap = cache->capacity;
-  a.bl = cache->block_len;
-  a.bl_shift = cache->block_len == 16 ? 4 : cache->block_len == 32 ? 5 : cache->block_len == 64 ? 6 : 7;
-  a.Q = Q;
-  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(mem->D)));
-  a.n_split = p.n_split;
-  a.loc_split = p.loc_split;
-  a.O = O;
-  a.lse = lse ? lse : track ? reinterpret_cast<float *>(ws + p.lse) : nullptr;
-  a.part_o = reinterpret_cast<float *>(ws + p.part_o);
-  a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
-  a.weights = track ? cache->weights : nullptr;
-  a.decay = weight_decay;
-  const int nt = attend8_nt(static_cast<int>(std::min<int64_t>(static_cast<int64_t>(tokens) * a.G, 64)));
-  return dispatch8(mem, cache->format, [&](auto t, auto d, auto f) {
-    using T = decltype(t);
-    const cudaStream_t st = to_stream(stream);
-    if (sizeof(T) == 4 || nt == 1) return launch_attend8<T, d.value, f.value, 1>(a, p, cache->batch, st);
-    if constexpr (sizeof(T) == 2) {
-      if (nt == 2) return launch_attend8<T, d.value, f.value, 2>(a, p, cache->batch, st);
-      return launch_attend8<T, d.value, f.value, 4>(a, p, cache->batch, st);
-    }
-    return MSA_OK;
-  });
+  return cache8_attend(mem, content, ids, nullptr, 0, k, cache, tokens, n_q_heads, Q, n_tokens, O,
+                       lse, weight_decay, workspace, workspace_bytes, to_stream(stream));
 }
 
 size_t msa_cache8_evict_workspace_size(const msa_memory *mem, const msa_cache8 *cache) {

@@ -123,6 +123,8 @@ SIGNATURES = {
     "msa_cache8_attend_workspace_size": (_SZ, [_P, _P, _I32, _I32, _I32]),
     "msa_cache8_attend": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P, _P,
                                          ctypes.c_float, _P, _SZ, _P]),
+    "msa_cache8_attend_fetched": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P, _P,
+                                                 ctypes.c_float, _P, _SZ, _P]),
     "msa_cache8_evict_workspace_size": (_SZ, [_P, _P]),
     "msa_cache8_evict": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _P, _SZ, _P]),
     "msa_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _P]),
@@ -697,7 +699,9 @@ class Cache8:
                stream=None):
         """Attention of the cache's newest tokens over the retrieved memory rows and the cached
         rows (msa_cache8_attend): Q, O [batch][tokens][n_q_heads][D], Q already rotated; lse
-        [batch][tokens][n_q_heads] optional.  weight_decay None leaves ``weights`` alone."""
+        [batch][tokens][n_q_heads] optional.  weight_decay None leaves ``weights`` alone.
+        ``content`` is the memory's pooled content, or the Fetcher that just fetched ``ids``
+        (msa_cache8_attend_fetched)."""
         mem, dev = self.mem, self.device.index
         if not isinstance(Q, torch.Tensor) or Q.dim() != 4:
             raise ValueError("Q: expected [batch][tokens][n_q_heads][D]")
@@ -706,9 +710,14 @@ class Cache8:
         k = ids.shape[1] if ids is not None else 0
         if weight_decay is not None and not weight_decay >= 0.0:
             raise ValueError(f"weight_decay must be >= 0 or None, got {weight_decay}")
-        _call(_lib.msa_cache8_attend, self.device, stream, mem.handle,
-              _tensor(content, "content", (mem.n_chunks, 2, mem.n_kv_heads, mem.head_dim), mem.dtype,
-                      dev) if k else None,
+        if isinstance(content, Fetcher):
+            fn, rows = _lib.msa_cache8_attend_fetched, content.handle
+        else:
+            fn, rows = _lib.msa_cache8_attend, None
+            if k:
+                rows = _tensor(content, "content", (mem.n_chunks, 2, mem.n_kv_heads, mem.head_dim),
+                               mem.dtype, dev)
+        _call(fn, self.device, stream, mem.handle, rows,
               _tensor(ids, "ids", (self.batch, k), torch.int32, dev) if k else None, k, self._ref,
               T, H_q, _tensor(Q, "Q", shape, mem.dtype, dev), self._counts(n_tokens, "n_tokens"),
               _tensor(O, "O", shape, mem.dtype, dev),
