@@ -590,7 +590,7 @@ class Rope:
         dtype = q.dtype
         qp, qh, qs = self._side(q, "q", lead, dtype)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=self.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
             qo, qoh, qos = q_out.data_ptr(), qh, qh * self.head_dim
         else:
             qo, qoh, qos = self._side(q_out, "q_out", lead, dtype)
@@ -598,7 +598,7 @@ class Rope:
         if k is not None:
             kp, kh, ks = self._side(k, "k", lead, dtype)
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=dtype, device=self.device)
+                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
                 ko, koh, kos = k_out.data_ptr(), kh, kh * self.head_dim
             else:
                 ko, koh, kos = self._side(k_out, "k_out", lead, dtype)
@@ -684,7 +684,7 @@ class Cache8:
         if K_out is None:
             K_out = torch.empty(shape, dtype=mem.dtype, device=self.device)
         if V_out is None:
-            V_out = torch.empty(shape, dtype=mem.dtype, device=self.device)
+            V_out = torch.empty_like(K_out)
         _call(_lib.msa_cache8_read, self.device, stream, mem.handle, self._ref,
               self._counts(begin, "begin"), rows,
               _tensor(K_out, "K_out", shape, mem.dtype, self.device.index),
