@@ -5,8 +5,9 @@ rounding is the same in any precision.  Attention bounds, per output, first orde
 u = 2^-23 (tensor-core sums may truncate):
   ds  = (D + 16) u A, A = max_j sum_d |q_d k_jd| / sqrt(D)          error of a score
   lse : ds + (rows + 8) u + 4 u |lse|
-  O   : (2 ds + 2^-11 + (rows + 16) u) sum_j p_j |v_j| + rows 2^-28 max|v|,
-        2^-11 the rounding of a weight to fp16, the last term weights below fp16's normal
+  O   : (2 ds + w + (rows + 16) u) sum_j p_j |v_j| + rows 2^-28 max|v|,
+        w the rounding of a weight, 2^-11 to fp16 (bf16 queries) and 2^-22 to an fp16 head and
+        tail (fp32 queries, whose Q is split alike: 2^-22 again, inside ds), the last term weights below fp16's normal
         range: half its smallest step, 2^-25, against weights kept at 2^11 2^(s - m) with m at
         most 8 above the largest score, 2^-25 2^-11 2^8 = 2^-28 of the largest weight;
         a bf16 output adds half a step, 2^-8 |O|
@@ -182,7 +183,8 @@ def run_attend(mem, content, cache, ref, ids, T, G, n, q_scale=1.0, decay=None, 
     nrow = cache.capacity + 4096
     ds = (D + 16) * U * amp
     tl = ds + (nrow + 8) * U + 4 * U * np.where(np.isfinite(wl), np.abs(wl), 0)
-    to = (2 * ds[..., None] + 2.0 ** -11 + (nrow + 16) * U) * pv + nrow * 2.0 ** -28 * vmax
+    w_round = 2.0 ** -11 if mem.dtype == torch.bfloat16 else 2.0 ** -22
+    to = (2 * ds[..., None] + w_round + (nrow + 16) * U) * pv + nrow * 2.0 ** -28 * vmax
     if mem.dtype == torch.bfloat16:
         to = to + 2.0 ** -8 * (np.abs(want) + to)
     for b in range(B):

@@ -27,6 +27,9 @@
 // 2^-28 of the largest.
 //   Memory rows are bf16 and go through bf16 MMAs; P is split there into a bf16
 // head and tail, two MMAs, so it loses nothing either.
+//   fp32 queries run the same kernel with Q and P split into an fp16 head and
+// tail, two MMAs each: 2^-22 of the column's largest element is lost, as fp32
+// sums lose anyway.  fp32 memory rows have a kernel of their own on CUDA cores.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -63,6 +66,7 @@ struct Attend8Args {
   int n_split, loc_split;
   void *O;
   float *lse;
+  float2 *ml;        // with weights: reference (log2 units) and 1 / sum of every column's softmax
   float *part_o, *part_ml;
   float *weights;
   float decay;
@@ -227,8 +231,8 @@ template <int D, int NT>
 struct Attend8Smem {
   static constexpr int kCols = 8 * NT;
   static constexpr int kQPitch = D + 8;  // elements of a column's row (16 bytes of padding)
-  static constexpr int kQ = 0;                                   // fp16, scaled
-  static constexpr int kQb = kQ + kCols * kQPitch * 2;           // bf16, as given
+  static constexpr int kQ = 0;                                   // fp16, scaled (its head of fp32)
+  static constexpr int kQb = kQ + kCols * kQPitch * 2;           // bf16, as given (fp16 tail of fp32)
   static constexpr int kColScale = kQb + kCols * kQPitch * 2;    // fp32 per column
   static constexpr int kMerge = kColScale + kCols * 4;
   static constexpr int kMergeBytes = kC8Warps * kCols * (D + 4) * 4;  // O, m, l
@@ -239,42 +243,54 @@ struct Attend8Smem {
   static int bytes(int table_cap) { return kTable + (2 * kMaxTopK + 1 + table_cap) * 4; }
 };
 
-// The columns [c0, c0 + 8 NT) of Q, one warp a column: bf16 as given, fp16 scaled by a power of
-// two to 1 <= max < 2, and that scale times scale_log2.  Columns past the query's tokens are zero.
-template <int D, int NT>
+// The columns [c0, c0 + 8 NT) of Q, one warp a column, scaled by a power of two to 1 <= max < 2 as
+// fp16, and that scale times scale_log2.  bf16: the column as given beside it, for the memory rows;
+// fp32: what the fp16 value leaves.  Columns past the query's tokens are zero.
+template <typename T, int D, int NT>
 __device__ __forceinline__ void load_q_columns(const Attend8Args &a, int b, int g, int c0, int n,
                                                uint8_t *sm) {
   using Sm = Attend8Smem<D, NT>;
-  __half *qh = reinterpret_cast<__half *>(sm + Sm::kQ);
-  __nv_bfloat16 *qb = reinterpret_cast<__nv_bfloat16 *>(sm + Sm::kQb);
+  __half *qh = reinterpret_cast<__half *>(sm + Sm::kQ), *q2 = reinterpret_cast<__half *>(sm + Sm::kQb);
   float *cs = reinterpret_cast<float *>(sm + Sm::kColScale);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   constexpr int E = D / 32;
   for (int c = warp; c < Sm::kCols; c += kC8Warps) {
     const int cc = c0 + c, t = col_token(a, cc);
-    using Raw = std::conditional_t<E == 4, uint2, uint32_t>;  // this lane's elements
-    Raw raw{};
-    if (t < n)
-      raw = *reinterpret_cast<const Raw *>(
-          static_cast<const __nv_bfloat16 *>(a.Q) +
-          ((static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc - t * a.G) * D + lane * E);
-    uint32_t w[E / 2], h[E / 2];
-    *reinterpret_cast<Raw *>(w) = raw;
+    const int64_t at = ((static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc - t * a.G) * D + lane * E;
+    using Half = std::conditional_t<E == 4, uint2, uint32_t>;  // this lane's elements in 16 bits
+    Half raw{};
     float x[E], amax = 0.0f;
+    if constexpr (sizeof(T) == 2) {
+      if (t < n) raw = *reinterpret_cast<const Half *>(static_cast<const __nv_bfloat16 *>(a.Q) + at);
+      const uint32_t *w = reinterpret_cast<const uint32_t *>(&raw);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      x[e] = __uint_as_float(w[e / 2] << 16);
-      x[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
-      amax = fmaxf(amax, fmaxf(finite_abs(x[e]), finite_abs(x[e + 1])));
+      for (int e = 0; e < E; e += 2) {
+        x[e] = __uint_as_float(w[e / 2] << 16);
+        x[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = t < n ? static_cast<const float *>(a.Q)[at + e] : 0.0f;
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e) amax = fmaxf(amax, finite_abs(x[e]));
     amax = warp_max(amax);
     // 2^ex <= amax < 2^(ex + 1), within [-126, 126] so that 2^-ex is a normal number too
     const int ex = amax == 0.0f ? 0 : max(1, min(253, __float_as_int(amax) >> 23)) - 127;
     const float inv = __int_as_float((127 - ex) << 23);
+    uint32_t h[E / 2];
 #pragma unroll
     for (int e = 0; e < E; e += 2) h[e / 2] = pack_f16x2(x[e] * inv, x[e + 1] * inv);
-    *reinterpret_cast<Raw *>(qb + c * Sm::kQPitch + lane * E) = raw;
-    *reinterpret_cast<Raw *>(qh + c * Sm::kQPitch + lane * E) = *reinterpret_cast<Raw *>(h);
+    if constexpr (sizeof(T) == 4) {
+      uint32_t *w = reinterpret_cast<uint32_t *>(&raw);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h[e / 2]));
+        w[e / 2] = pack_f16x2(x[e] * inv - y.x, x[e + 1] * inv - y.y);
+      }
+    }
+    *reinterpret_cast<Half *>(qh + c * Sm::kQPitch + lane * E) = *reinterpret_cast<Half *>(h);
+    *reinterpret_cast<Half *>(q2 + c * Sm::kQPitch + lane * E) = raw;
     if (lane == 0) cs[c] = a.scale_log2 * __int_as_float((127 + ex) << 23);
   }
 }
@@ -366,6 +382,13 @@ __device__ __forceinline__ int column_rows(const Attend8Args &a, const Attend8Qu
   return t < q.n ? q.len - q.n + t + 1 : 0;
 }
 
+// A column's log-sum, and for the weights its reference and the reciprocal of its sum (a column that
+// sees nothing: an infinite reference, so that every weight is 0).
+__device__ __forceinline__ void write_stats(const Attend8Args &a, int64_t row, float M, float L) {
+  if (a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
+  if (a.ml) a.ml[row] = L == 0.0f ? make_float2(INFINITY, 0.0f) : make_float2(M, 1.0f / L);
+}
+
 // The CTA's warps (rows of `merge`: [warp][col][D outputs, m, l]) into O and lse, or into the
 // split's partial result.
 template <typename T, int D, int COLS>
@@ -389,7 +412,7 @@ __device__ __forceinline__ void merge_warps(const Attend8Args &a, const Attend8Q
     const int64_t row = (static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc - t * a.G;
     if (a.n_split == 1) {
       static_cast<T *>(a.O)[row * D + d] = Elem<T>::from_f(L == 0.0f ? 0.0f : o / L);
-      if (d == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
+      if (d == 0) write_stats(a, row, M, L);
     } else {
       a.part_o[(row * a.n_split + split) * D + d] = o;
       if (d == 0) {
@@ -400,10 +423,11 @@ __device__ __forceinline__ void merge_warps(const Attend8Args &a, const Attend8Q
   }
 }
 
-// grid (B * H_kv, n_split, column tiles), block 32 * kC8Warps.
-template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(32 * kC8Warps, NT == 1 ? 4 : NT == 2 ? 3 : 2)
+// grid (B * H_kv, splits, column tiles), block 32 * kC8Warps.  fp32: the local splits alone.
+template <typename T, int D, int NT, int FMT>
+__global__ void __launch_bounds__(32 * kC8Warps, (sizeof(T) == 4 ? 2 : 1) * NT == 1 ? 4 : (sizeof(T) == 4 ? 2 : 1) * NT == 2 ? 3 : 2)
 cache8_attend_kernel(Attend8Args a) {
+  constexpr bool F32 = sizeof(T) == 4;
   using Sm = Attend8Smem<D, NT>;
   constexpr int KS = D / 16;  // k steps of S^T
   constexpr bool kQRegs = NT <= 2;  // Q's fragments stay in registers
@@ -444,17 +468,18 @@ cache8_attend_kernel(Attend8Args a) {
     ksc = ks[(tile * 16) >> a.bl_shift];
     vsc = vs[(tile * 16) >> a.bl_shift];
   }
-  load_q_columns<D, NT>(a, b, g, c0, q.n, sm);
+  load_q_columns<T, D, NT>(a, b, g, c0, q.n, sm);
   int *pre = reinterpret_cast<int *>(sm + Sm::kTable), *base = pre + kMaxTopK + 1;
   int *table = base + kMaxTopK;
   int n_mem = 0;
-  if (a.k > 0 && (!own_mem || split >= a.loc_split))
+  if (!F32 && a.k > 0 && (!own_mem || split >= a.loc_split))
     n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
                               a.slots ? a.slots + static_cast<int64_t>(b) * a.k : nullptr, a.slot_chunks, table, pre, base, a.table_cap);
   __syncthreads();
 
   const __half *qh = reinterpret_cast<const __half *>(sm + Sm::kQ);
   const float *cs = reinterpret_cast<const float *>(sm + Sm::kColScale);
+  const __half *ql = reinterpret_cast<const __half *>(sm + Sm::kQb);  // fp32: the tails
   uint32_t qf[kQRegs ? NT : 1][KS][2];
   if constexpr (kQRegs) {
 #pragma unroll
@@ -507,6 +532,10 @@ cache8_attend_kernel(Attend8Args a) {
           const uint2 x = *reinterpret_cast<const uint2 *>(qh + (8 * nt + lg) * Sm::kQPitch + k_elem(i, lt));
           mma_f16_16816(s[nt], a0, a1, a2, a3, x.x, x.y);
         }
+        if constexpr (F32) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(ql + (8 * nt + lg) * Sm::kQPitch + k_elem(i, lt));
+          mma_f16_16816(s[nt], a0, a1, a2, a3, x.x, x.y);
+        }
       }
     }
     const float k_scale = ksc, v_scale = vsc;
@@ -529,12 +558,19 @@ cache8_attend_kernel(Attend8Args a) {
     st.step(s);
     st.raise_unit(v_scale);
     const float ratio = v_scale * st.inv_unit;
-    uint32_t pb[NT][2];
+    uint32_t pb[NT][2], pt[F32 ? NT : 1][2];  // P, and of fp32 its tail
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      pb[nt][0] = movmatrix_trans(pack_f16x2(s[nt][0] * ratio, s[nt][1] * ratio));
-      pb[nt][1] = movmatrix_trans(pack_f16x2(s[nt][2] * ratio, s[nt][3] * ratio));
-    }
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float p0 = s[nt][2 * r] * ratio, p1 = s[nt][2 * r + 1] * ratio;
+        const uint32_t head = pack_f16x2(p0, p1);
+        pb[nt][r] = movmatrix_trans(head);
+        if constexpr (F32) {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&head));
+          pt[nt][r] = movmatrix_trans(pack_f16x2(p0 - y.x, p1 - y.y));
+        }
+      }
     VTile<D> vt;
     vt.from_shared(at + Tile8<D>::kBytes, lane);
     if (FMT == MSA_CACHE_E4M3 && x0 + 16 > n_loc) vt.clear_from(lane, n_loc - x0);
@@ -552,13 +588,18 @@ cache8_attend_kernel(Attend8Args a) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
           mma_f16_16816(st.acc[nt][2 * w + i], lo[0][i], hi[0][i], lo[1][i], hi[1][i], pb[nt][0],
                         pb[nt][1]);
+          if constexpr (F32)
+            mma_f16_16816(st.acc[nt][2 * w + i], lo[0][i], hi[0][i], lo[1][i], hi[1][i], pt[nt][0],
+                          pt[nt][1]);
+        }
     }
   }
 
-  // ---- memory rows: every column sees them
+  // ---- memory rows: every column sees them (fp32 ones have a kernel of their own)
+  if constexpr (!F32) {
   const int nm = (n_mem + 15) / 16;
   const int ms = own_mem ? split - a.loc_split : split, mn = own_mem ? a.n_split - a.loc_split : a.n_split;
   const int m1 = share(nm, ms + 1, mn);
@@ -631,6 +672,7 @@ cache8_attend_kernel(Attend8Args a) {
       }
     }
   }
+  }
 
   // ---- the warps meet
   cp_async_wait<0>();
@@ -657,69 +699,48 @@ cache8_attend_kernel(Attend8Args a) {
       }
     }
   __syncthreads();
-  merge_warps<__nv_bfloat16, D, Sm::kCols>(a, q, b, g, c0, split, merge);
+  merge_warps<T, D, Sm::kCols>(a, q, b, g, c0, split, merge);
 }
 
-// ---------------------------------------------------------------- fp32
-// Memories of fp32: CUDA cores, four columns a CTA.  Scores with a lane on each of 32 context
-// rows, outputs with a lane on D / 32 elements; sums in fp32.
+// ---------------------------------------------------------------- fp32 memory rows
+// CUDA cores, four columns a CTA: scores with a lane on each of 32 rows, outputs with a lane on
+// D / 32 elements; sums in fp32.  grid (B * H_kv, memory splits, ceil(columns / 4)).
 constexpr int kC8Cols32 = 4;
-// acc + sum of 16 products, one factor from shared memory (16-byte aligned)
-__device__ __forceinline__ float dot16(const float *q, const float x[16], float acc) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 y = *reinterpret_cast<const float4 *>(q + 4 * i);
-    acc = fmaf(y.x, x[4 * i], acc);
-    acc = fmaf(y.y, x[4 * i + 1], acc);
-    acc = fmaf(y.z, x[4 * i + 2], acc);
-    acc = fmaf(y.w, x[4 * i + 3], acc);
-  }
-  return acc;
-}
 template <int D>
-struct Attend8Smem32 {
+struct Memory8Smem {
   static constexpr int kQ = 0;
   static constexpr int kMerge = kQ + kC8Cols32 * D * 4;
   static constexpr int kTable = kMerge + kC8Warps * kC8Cols32 * (D + 4) * 4;
   static int bytes(int table_cap) { return kTable + (2 * kMaxTopK + 1 + table_cap) * 4; }
 };
 
-template <int D, int FMT>
+template <int D>
 __global__ void __launch_bounds__(32 * kC8Warps)
-cache8_attend_f32_kernel(Attend8Args a) {
-  using Sm = Attend8Smem32<D>;
+cache8_memory_f32_kernel(Attend8Args a) {
+  using Sm = Memory8Smem<D>;
   constexpr int C = kC8Cols32, E = D / 32;
   extern __shared__ __align__(16) uint8_t sm[];
-  const int b = blockIdx.x / a.H_kv, g = blockIdx.x % a.H_kv, split = blockIdx.y;
+  const int b = blockIdx.x / a.H_kv, g = blockIdx.x % a.H_kv;
   const int c0 = blockIdx.z * C;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   griddep_wait();
   griddep_launch();
-  const Attend8Query q = attend8_query(a, b, blockIdx.x % a.H_kv == 0 && split == 0 && c0 == 0 &&
-                                                 threadIdx.x == 0);
-  if (c0 / a.G >= q.n) return;
+  const Attend8Query q = attend8_query(a, b, false);
+  if (col_token(a, c0) >= q.n) return;
   float *qs = reinterpret_cast<float *>(sm + Sm::kQ);
   for (int i = threadIdx.x; i < C * D; i += 32 * kC8Warps) {
-    const int cc = c0 + i / D, t = cc / a.G;
+    const int cc = c0 + i / D, t = col_token(a, cc);
     qs[i] = t < q.n ? static_cast<const float *>(a.Q)[((static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G +
-                                                       g * a.G + cc % a.G) * D + i % D] * a.scale_log2
+                                                       g * a.G + cc - t * a.G) * D + i % D] * a.scale_log2
                     : 0.0f;
   }
   int *pre = reinterpret_cast<int *>(sm + Sm::kTable), *base = pre + kMaxTopK + 1;
   int *table = base + kMaxTopK;
-  int n_mem = 0;
-  if (a.k > 0)
-    n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
-                              a.slots ? a.slots + static_cast<int64_t>(b) * a.k : nullptr, a.slot_chunks, table, pre, base, a.table_cap);
+  const int n_mem = build_chunk_table(a.ids + static_cast<int64_t>(b) * a.k, a.k, a.doc_chunk_off, a.n_docs,
+                                      a.slots ? a.slots + static_cast<int64_t>(b) * a.k : nullptr,
+                                      a.slot_chunks, table, pre, base, a.table_cap);
   __syncthreads();
-  const int last_col = min(c0 + C, q.n * a.G) - 1;
-  const int n_loc = max(0, column_rows(a, q, last_col));
-  const int nl = (n_loc + 31) / 32, nm = (n_mem + 31) / 32, n = nl + nm;  // shares of both
-  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
   const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
-  int rows[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) rows[c] = c0 + c <= last_col ? column_rows(a, q, c0 + c) : 0;
   float m[C], l[C], acc[C][E];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -728,76 +749,47 @@ cache8_attend_f32_kernel(Attend8Args a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[c][e] = 0.0f;
   }
-  const int i1 = share(n, split + 1, a.n_split);
-  for (int i = share(n, split, a.n_split) + warp; i < i1; i += kC8Warps) {
-    const bool loc = i < nl;
-    const int x0 = (loc ? i : i - nl) * 32, x = x0 + lane;
-    const int lim = loc ? n_loc : n_mem;
+  const int nm = (n_mem + 31) / 32, own = a.n_split - a.loc_split, part = blockIdx.y;
+  const int i1 = share(nm, part + 1, own);
+  for (int i = share(nm, part, own) + warp; i < i1; i += kC8Warps) {
+    const int x0 = i * 32, x = x0 + lane;
     float s[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) s[c] = 0.0f;
-    if (x < lim) {
-      if (loc) {
-        const uint8_t *kr = a.k8 + (bh * a.cap + x) * D;
-        const float sc = a.ks[bh * (a.cap / a.bl) + x / a.bl];
-#pragma unroll 2
-        for (int p = 0; p < D / 16; ++p) {
-          float kx[16];
-          unpack16<FMT>(*reinterpret_cast<const uint4 *>(kr + 16 * p), sc, kx);
+    if (x < n_mem) {
+      const float *kr = static_cast<const float *>(a.content) + static_cast<int64_t>(table[x]) * 2 * kv + g * D;
+#pragma unroll 4
+      for (int p = 0; p < D / 4; ++p) {
+        const float4 k = *reinterpret_cast<const float4 *>(kr + 4 * p);
 #pragma unroll
-          for (int c = 0; c < C; ++c) s[c] = dot16(qs + c * D + 16 * p, kx, s[c]);
-        }
-      } else {
-        const float *kr = static_cast<const float *>(a.content) + static_cast<int64_t>(table[x]) * 2 * kv + g * D;
-#pragma unroll 2
-        for (int p = 0; p < D / 4; ++p) {
-          float kx[4];
-          load4(kr + 4 * p, kx);
-#pragma unroll
-          for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[c] = fmaf(qs[c * D + 4 * p + e], kx[e], s[c]);
+        for (int c = 0; c < C; ++c) {
+          const float4 y = *reinterpret_cast<const float4 *>(qs + c * D + 4 * p);
+          s[c] = fmaf(y.x, k.x, fmaf(y.y, k.y, fmaf(y.z, k.z, fmaf(y.w, k.w, s[c]))));
         }
       }
     }
-    float f[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const bool see = loc ? x < rows[c] : (x < lim && c0 + c <= last_col);
-      if (!see) s[c] = -INFINITY;
+      if (x >= n_mem) s[c] = -INFINITY;
       const float mn = fmaxf(m[c], warp_max(s[c]));
       const float ref = mn == -INFINITY ? 0.0f : mn;
-      f[c] = mn == -INFINITY ? 1.0f : exp2f(m[c] - mn);
+      const float f = mn == -INFINITY ? 1.0f : exp2f(m[c] - mn);
       m[c] = mn;
       s[c] = exp2f(s[c] - ref);
-      l[c] = l[c] * f[c] + s[c];
+      l[c] = l[c] * f + s[c];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[c][e] *= f[c];
+      for (int e = 0; e < E; ++e) acc[c][e] *= f;
     }
     // eight rows of V in flight; rows past the last one have weight 0 and read the last one
-    const int last = lim - 1 - x0;
+    const int last = n_mem - 1 - x0;
     for (int r0 = 0; r0 <= min(31, last); r0 += 8) {
-      float v[8][4];
+      float v[8][E];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int r = x0 + min(r0 + u, last);
-        if (loc) {
-          const uint8_t *vr = a.v8 + (bh * a.cap + r) * D + E * lane;
-          const float sc = a.vs[(bh * a.cap + r) >> a.bl_shift];
-          uint32_t w;
-          if constexpr (E == 4)
-            w = *reinterpret_cast<const uint32_t *>(vr);
-          else
-            w = *reinterpret_cast<const uint16_t *>(vr);
-          Fmt8<FMT>::unpack4(w, v[u]);
+        const float *vr = static_cast<const float *>(a.content) +
+                          static_cast<int64_t>(table[x0 + min(r0 + u, last)]) * 2 * kv + kv + g * D + E * lane;
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[u][e] *= sc;
-        } else {
-          const float *vr = static_cast<const float *>(a.content) +
-                            static_cast<int64_t>(table[r]) * 2 * kv + kv + g * D + E * lane;
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[u][e] = vr[e];
-        }
+        for (int e = 0; e < E; ++e) v[u][e] = vr[e];
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u)
@@ -823,7 +815,7 @@ cache8_attend_f32_kernel(Attend8Args a) {
     }
   }
   __syncthreads();
-  merge_warps<float, D, C>(a, q, b, g, c0, split, merge);
+  merge_warps<float, D, C>(a, q, b, g, c0, a.loc_split + part, merge);
 }
 
 // ---------------------------------------------------------------- combine
@@ -890,52 +882,52 @@ cache8_combine_kernel(Attend8Args a, int rows) {
     out[0] = Elem<T>::from_f(o[0]);
     out[1] = Elem<T>::from_f(o[1]);
   }
-  if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) / kLog2e;
+  if (lane == 0) write_stats(a, row, M, L);
 }
 
 // ---------------------------------------------------------------- weights
-// The weight each cached row received: with the softmax's log-sum known, a second pass over K
-// alone recomputes the scores, p = 2^(s - lse), and sums them over the columns, 8 NT at a time with
+// The weight each cached row received: with the softmax's reference m and sum L known, a second pass
+// over K alone recomputes the scores, p = 2^(s - m) / L, and sums them over the columns, 8 NT at a time with
 // Q's fragments in registers.  Few columns (one round of 8 NT): bound by K's bytes; a warp streams
 // its tiles through a ring.  More: a CTA copies kC8wRows rows to shared memory once and walks over
 // all columns, its tiles' sums in registers.
-// grid (CTAs a head, B * H_kv), block 32 * kC8Warps.  fp32 memories: see below.
+// grid (CTAs a head, B * H_kv), block 32 * kC8Warps.
 constexpr int kC8wTiles = 4;                              // 16-row tiles a warp, or its ring
 constexpr int kC8wRows = 16 * kC8wTiles * kC8Warps;
 template <int D, int NT>
 struct Weight8Smem {
   static constexpr int kK = Attend8Smem<D, NT>::kMerge;   // behind Q and its scales
-  static constexpr int kLse = kK + kC8wRows * D;
-  static constexpr int kBytes = kLse + 8 * NT * 4;
+  static constexpr int kStats = kK + kC8wRows * D;
+  static constexpr int kBytes = kStats + 8 * NT * 8;
 };
 
 // Columns [c0, c0 + 8 NT) as a lane holds them, and the weights they give a tile's rows.
-template <int D, int NT, int FMT>
+template <typename T, int D, int NT, int FMT>
 struct WeightColumns {
   static constexpr int KS = D / 16;
   uint32_t qf[NT][KS][2];
-  float cf[NT][2], ls[NT][2];
+  float cf[NT][2];
+  float2 ml[NT][2];
   int rows[NT][2], all_see;
+  const __half *tail;  // fp32: Q's tails, in shared memory
 
-  // Q, its scales and the log-sums to shared memory and from there to registers (all warps)
+  // Q, its scales and the softmaxes' statistics to shared memory and from there to registers (all
+  // warps)
   __device__ __forceinline__ void load(const Attend8Args &a, const Attend8Query &q, int b, int g,
-                                       int c0, uint8_t *sm, float *lse2) {
+                                       int c0, uint8_t *sm, float2 *stats) {
     using Sm = Attend8Smem<D, NT>;
     const int lane = threadIdx.x % 32, lg = lane >> 2, lt = lane & 3;
-    load_q_columns<D, NT>(a, b, g, c0, q.n, sm);
+    load_q_columns<T, D, NT>(a, b, g, c0, q.n, sm);
     for (int c = threadIdx.x; c < Sm::kCols; c += 32 * kC8Warps) {
       const int cc = c0 + c, t = col_token(a, cc);
-      float v = INFINITY;  // no token, or one that sees nothing: weight 0
-      if (t < q.n) {
-        const float x = a.lse[(static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc - t * a.G];
-        if (x != -INFINITY) v = x * kLog2e;
-      }
-      lse2[c] = v;
+      stats[c] = t < q.n ? a.ml[(static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc - t * a.G]
+                         : make_float2(INFINITY, 0.0f);  // no token: weight 0
     }
     __syncthreads();
     const __half *qh = reinterpret_cast<const __half *>(sm + Sm::kQ);
     const float *cs = reinterpret_cast<const float *>(sm + Sm::kColScale);
     all_see = column_rows(a, q, c0);
+    tail = reinterpret_cast<const __half *>(sm + Sm::kQb) + lg * Sm::kQPitch;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -948,7 +940,7 @@ struct WeightColumns {
       for (int h = 0; h < 2; ++h) {
         const int c = 8 * nt + 2 * lt + h;
         cf[nt][h] = cs[c];
-        ls[nt][h] = lse2[c];
+        ml[nt][h] = stats[c];
         rows[nt][h] = column_rows(a, q, c0 + c);
       }
     }
@@ -969,26 +961,32 @@ struct WeightColumns {
       widen4<FMT>(kt.w[0][k], a0, a2);
       widen4<FMT>(kt.w[1][k], a1, a3);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
+        if constexpr (sizeof(T) == 4) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(tail + 8 * nt * Attend8Smem<D, NT>::kQPitch + k_elem(k, lane & 3));
+          mma_f16_16816(s[nt], a0, a1, a2, a3, x.x, x.y);
+        }
+      }
     }
     const bool masked = x0 + 16 > all_see;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float p = ex2_approx(s[nt][e] * (cf[nt][e & 1] * k_scale) - ls[nt][e & 1]);
+        float p = ex2_approx(s[nt][e] * (cf[nt][e & 1] * k_scale) - ml[nt][e & 1].x);
         if (masked && x0 + lg + 8 * (e >> 1) >= rows[nt][e & 1]) p = 0.0f;
-        sum[e >> 1] += p;
+        sum[e >> 1] = fmaf(p, ml[nt][e & 1].y, sum[e >> 1]);
       }
   }
 };
 
-template <int D, int NT, int FMT>
+template <typename T, int D, int NT, int FMT>
 __global__ void __launch_bounds__(32 * kC8Warps)
 cache8_weight_kernel(Attend8Args a, int stream) {
   using Wm = Weight8Smem<D, NT>;
   extern __shared__ __align__(16) uint8_t sm[];
-  float *lse2 = reinterpret_cast<float *>(sm + Wm::kLse);
+  float2 *stats = reinterpret_cast<float2 *>(sm + Wm::kStats);
   griddep_wait();
   griddep_launch();
   const int b = blockIdx.y / a.H_kv, g = blockIdx.y % a.H_kv;
@@ -997,7 +995,7 @@ cache8_weight_kernel(Attend8Args a, int stream) {
   const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
   const int tiles = (q.len + 15) / 16, cols = q.n * a.G;
   const uint32_t ring = smem_u32(sm + Wm::kK) + warp * kC8wTiles * Tile8<D>::kBytes;
-  WeightColumns<D, NT, FMT> col;
+  WeightColumns<T, D, NT, FMT> col;
   auto fetch = [&](int slot, int tile) {
     const uint8_t *src = a.k8 + (bh * a.cap + tile * 16) * D;
 #pragma unroll
@@ -1029,7 +1027,7 @@ cache8_weight_kernel(Attend8Args a, int stream) {
       cp_async_commit();
       ahead += step;
     }
-    col.load(a, q, b, g, 0, sm, lse2);
+    col.load(a, q, b, g, 0, sm, stats);
     float k_scale = tile < tiles ? scale_of(tile) : 0.0f;
     for (int slot = 0; tile < tiles; tile += step) {
       cp_async_wait<kC8wTiles - 2>();
@@ -1064,7 +1062,7 @@ cache8_weight_kernel(Attend8Args a, int stream) {
   __syncwarp();
   for (int c0 = 0; c0 < cols; c0 += 8 * NT) {
     if (c0) __syncthreads();
-    col.load(a, q, b, g, c0, sm, lse2);
+    col.load(a, q, b, g, c0, sm, stats);
 #pragma unroll
     for (int i = 0; i < kC8wTiles; ++i)
       if (tile_of(i) < tiles) col.add(ring + i * Tile8<D>::kBytes, tile_of(i) * 16, k_scale[i], sum[i]);
@@ -1072,55 +1070,6 @@ cache8_weight_kernel(Attend8Args a, int stream) {
 #pragma unroll
   for (int i = 0; i < kC8wTiles; ++i)
     if (tile_of(i) < tiles) write(tile_of(i), sum[i]);
-}
-
-// The same on CUDA cores: a lane on each of 32 rows, Q broadcast from shared memory.
-template <int D, int FMT>
-__global__ void __launch_bounds__(32 * kC8Warps)
-cache8_weight_f32_kernel(Attend8Args a) {
-  __shared__ __align__(16) float qs[kC8Cols32 * D];
-  __shared__ float lse2[kC8Cols32];
-  griddep_wait();
-  griddep_launch();
-  const int b = blockIdx.y / a.H_kv, g = blockIdx.y % a.H_kv;
-  const Attend8Query q = attend8_query(a, b, false);
-  const int x = blockIdx.x * 32 * kC8Warps + threadIdx.x;
-  if (static_cast<int>(blockIdx.x) * 32 * kC8Warps >= q.len) return;
-  const int64_t bh = static_cast<int64_t>(b) * a.H_kv + g;
-  const bool work = x < q.len;
-  const uint8_t *kr = a.k8 + (bh * a.cap + (work ? x : 0)) * D;
-  const float sc = work ? a.ks[bh * (a.cap / a.bl) + x / a.bl] : 0.0f;
-  float sum = 0.0f;
-  for (int c0 = 0; c0 < q.n * a.G; c0 += kC8Cols32) {
-    if (c0) __syncthreads();
-    for (int i = threadIdx.x; i < kC8Cols32 * D; i += 32 * kC8Warps) {
-      const int cc = c0 + i / D, t = cc / a.G;
-      const int64_t row = (static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + cc % a.G;
-      qs[i] = t < q.n ? static_cast<const float *>(a.Q)[row * D + i % D] * a.scale_log2 : 0.0f;
-      if (i % D == 0) {
-        float v = INFINITY;
-        if (t < q.n && a.lse[row] != -INFINITY) v = a.lse[row] * kLog2e;
-        lse2[i / D] = v;
-      }
-    }
-    __syncthreads();
-    if (!work) continue;
-    float s[kC8Cols32] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-    for (int p = 0; p < D / 16; ++p) {
-      float kx[16];
-      unpack16<FMT>(*reinterpret_cast<const uint4 *>(kr + 16 * p), sc, kx);
-#pragma unroll
-      for (int c = 0; c < kC8Cols32; ++c) s[c] = dot16(qs + c * D + 16 * p, kx, s[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < kC8Cols32; ++c)
-      sum += x < column_rows(a, q, c0 + c) ? exp2f(s[c] - lse2[c]) : 0.0f;
-  }
-  if (work) {
-    float *w = a.weights + bh * a.cap + x;
-    *w = a.decay == 0.0f ? sum : a.decay * *w + sum;
-  }
 }
 
 }  // namespace msa

@@ -576,7 +576,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     if (real) {
       const float l = l_run * exp2f(-kC8Shift);
       if (one) {
-        if (a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (m_run + log2f(l)) / kLog2e;
+        write_stats(a, orow, m_run, l);
       } else {
         a.part_ml[(orow * a.n_split + split) * 2] = m_run;
         a.part_ml[(orow * a.n_split + split) * 2 + 1] = l;

@@ -231,22 +231,23 @@ msa_status dispatch8(const msa_memory *mem, int format, F &&f) {
 }
 
 // Columns (token, head) of one kv head share an MMA's 8, 16 or 32 columns; more go to further CTAs.
-int attend8_nt(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
+// (fp32 at most 16: its heads and tails take twice the registers)
+int attend8_nt(msa_dtype t, int64_t cols) { return cols <= 8 ? 1 : cols <= 16 || t == MSA_F32 ? 2 : 4; }
 
 struct Attend8Plan {
   int n_split = 1, loc_split = 1, col_tiles = 1, table_cap = 0;
   bool tc = false;  // tcgen05: col_tiles is then the number of tile pairs
-  size_t part_o = 0, part_ml = 0, lse = 0, bytes = 0;
+  size_t part_o = 0, part_ml = 0, ml = 0, bytes = 0;
 };
 
-// Partial results of the splits, and the log-sums where weights are tracked without `lse`.
+// Partial results of the splits, and the softmaxes' statistics where weights are tracked.
 void plan_attend8_scratch(Attend8Plan &p, const msa_memory *mem, const msa_cache8 *c, size_t rows) {
   if (p.n_split > 1) {
     p.part_ml = round256(rows * p.n_split * mem->D * 4);
     p.bytes = p.part_ml + round256(rows * p.n_split * 2 * 4);
   }
-  p.lse = p.bytes;
-  if (c->weights) p.bytes += round256(rows * 4);
+  p.ml = p.bytes;
+  if (c->weights) p.bytes += round256(rows * 8);
 }
 
 // Columns (tokens * heads of a group) from which the tcgen05 kernel takes over.  It widens every
@@ -282,8 +283,7 @@ Attend8Plan plan_attend8(const msa_memory *mem, const msa_cache8 *c, int T, int 
     plan_attend8_scratch(p, mem, c, rows);
     return p;
   }
-  const int per = mem->dtype == MSA_BF16 ? 8 * attend8_nt(static_cast<int>(std::min<int64_t>(cols, 64)))
-                                         : msa::kC8Cols32;
+  const int per = 8 * attend8_nt(mem->dtype, cols);
   p.col_tiles = static_cast<int>((cols + per - 1) / per);
   const int64_t ctas = bh * p.col_tiles;
   // Splits of at most 2,048 local rows, so that ragged lengths spread over the SMs (64 queries of
@@ -292,11 +292,11 @@ Attend8Plan plan_attend8(const msa_memory *mem, const msa_cache8 *c, int T, int 
   // is split, the memory rows get splits of their own, so that the others need no chunk table; a
   // memory row counts as two local ones (bf16 against one byte).
   const bool bf16 = mem->dtype == MSA_BF16;
-  const int64_t room = static_cast<int64_t>(num_sms()) * (!bf16 || per == 8 ? 4 : per == 16 ? 3 : 2);
+  const int64_t room = static_cast<int64_t>(num_sms()) * (per * (bf16 ? 1 : 2) == 8 ? 4 : per * (bf16 ? 1 : 2) == 16 ? 3 : 2);
   int64_t loc = (c->capacity + 2047) / 2048, own = 0;
   const bool fill = ctas * (loc + (max_mem > 0 ? 1 : 0)) < room;
   if (fill) loc = std::max<int64_t>(1, room / ctas);
-  if (bf16 && max_mem > 0 && loc > 1) {
+  if (max_mem > 0 && (loc > 1 || !bf16)) {  // (fp32 memory rows are a kernel's of their own)
     own = std::max<int64_t>(1, loc * 2 * max_mem / (2 * max_mem + c->capacity));
     own = std::min<int64_t>(std::min<int64_t>(own, (max_mem + 63) / 64), msa::kC8MaxSplit - 64);
     if (fill) loc = std::max<int64_t>(1, loc - own);
@@ -341,44 +341,43 @@ msa_status launch_prefill8(const msa::Attend8Args &a, const Attend8Plan &p, int 
 template <typename T, int D, int FMT, int NT>
 msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B, cudaStream_t st) {
   constexpr bool kBf16 = sizeof(T) == 2;
-  const dim3 grid(B * a.H_kv, p.n_split, p.col_tiles), block(32 * msa::kC8Warps);
-  void (*kern)(msa::Attend8Args);
-  int smem;
-  if constexpr (kBf16) {
-    kern = msa::cache8_attend_kernel<D, NT, FMT>;
-    smem = msa::Attend8Smem<D, NT>::bytes(p.table_cap);
-  } else {
-    kern = msa::cache8_attend_f32_kernel<D, FMT>;
-    smem = msa::Attend8Smem32<D>::bytes(p.table_cap);
-  }
+  const dim3 block(32 * msa::kC8Warps);
+  const int own = p.n_split - p.loc_split;
   if (kBf16 && D == 128 && p.tc) {
     const msa_status s = launch_prefill8<FMT>(a, p, B, st);
     if (s != MSA_OK) return s;
   } else {
+    auto kern = msa::cache8_attend_kernel<T, D, NT, FMT>;
+    const int smem = msa::Attend8Smem<D, NT>::bytes(kBf16 ? p.table_cap : 0);
     MSA_CUDA(allow_smem(kern, smem));
-    MSA_CUDA(launch_pdl(kern, grid, block, smem, st, a));
+    MSA_CUDA(launch_pdl(kern, dim3(B * a.H_kv, kBf16 ? p.n_split : p.loc_split, p.col_tiles), block, smem,
+                        st, a));
     MSA_LAUNCHED("cache8_attend_kernel");
+    if (!kBf16 && own > 0) {
+      auto mk = msa::cache8_memory_f32_kernel<D>;
+      const int ms = msa::Memory8Smem<D>::bytes(p.table_cap);
+      const int tiles = (a.T * a.G + msa::kC8Cols32 - 1) / msa::kC8Cols32;
+      MSA_CUDA(allow_smem(mk, ms));
+      MSA_CUDA(launch_pdl(mk, dim3(B * a.H_kv, own, tiles), block, ms, st, a));
+      MSA_LAUNCHED("cache8_memory_f32_kernel");
+    }
   }
   if (p.n_split > 1) {
-    MSA_CUDA(launch_pdl(msa::cache8_combine_kernel<T, D>,
-                        dim3(static_cast<unsigned>((static_cast<int64_t>(B) * a.T * a.H_kv * a.G + 3) / 4)),
-                        dim3(128), 0, st, a, B * a.T * a.H_kv * a.G));
+    const int rows = B * a.T * a.H_kv * a.G;
+    MSA_CUDA(launch_pdl(msa::cache8_combine_kernel<T, D>, dim3((static_cast<unsigned>(rows) + 3) / 4),
+                        dim3(128), 0, st, a, rows));
     MSA_LAUNCHED("cache8_combine_kernel");
   }
   if (a.weights) {
-    if constexpr (kBf16) {
-      auto wk = msa::cache8_weight_kernel<D, NT, FMT>;
-      const int ws = msa::Weight8Smem<D, NT>::kBytes;
-      MSA_CUDA(allow_smem(wk, ws));
-      // one round of columns: a CTA streams its share of the tiles, about eight CTAs an SM in all
-      // (a CTA's set-up takes as long as a dozen tiles); more rounds: a CTA for every kC8wRows rows
-      const int chunks = (a.cap + msa::kC8wRows - 1) / msa::kC8wRows;
-      const bool stream = static_cast<int64_t>(a.T) * a.G <= 8 * NT;
-      const int grid_x = stream ? std::min(chunks, (8 * num_sms() + B * a.H_kv - 1) / (B * a.H_kv)) : chunks;
-      MSA_CUDA(launch_pdl(wk, dim3(grid_x, B * a.H_kv), block, ws, st, a, stream ? 1 : 0));
-    } else
-      MSA_CUDA(launch_pdl(msa::cache8_weight_f32_kernel<D, FMT>,
-                          dim3((a.cap + 127) / 128, B * a.H_kv), block, 0, st, a));
+    auto wk = msa::cache8_weight_kernel<T, D, NT, FMT>;
+    const int ws = msa::Weight8Smem<D, NT>::kBytes;
+    MSA_CUDA(allow_smem(wk, ws));
+    // one round of columns: a CTA streams its share of the tiles, about eight CTAs an SM in all
+    // (a CTA's set-up takes as long as a dozen tiles); more rounds: a CTA for every kC8wRows rows
+    const int chunks = (a.cap + msa::kC8wRows - 1) / msa::kC8wRows;
+    const bool stream = static_cast<int64_t>(a.T) * a.G <= 8 * NT;
+    const int grid_x = stream ? std::min(chunks, (8 * num_sms() + B * a.H_kv - 1) / (B * a.H_kv)) : chunks;
+    MSA_CUDA(launch_pdl(wk, dim3(grid_x, B * a.H_kv), block, ws, st, a, stream ? 1 : 0));
     MSA_LAUNCHED("cache8_weight_kernel");
   }
   return MSA_OK;
@@ -445,20 +444,19 @@ msa_status msa_host::cache8_attend(const msa_memory *mem, const void *content, c
   a.n_split = p.n_split;
   a.loc_split = p.loc_split;
   a.O = O;
-  a.lse = lse ? lse : track ? reinterpret_cast<float *>(ws + p.lse) : nullptr;
+  a.lse = lse;
+  a.ml = track ? reinterpret_cast<float2 *>(ws + p.ml) : nullptr;
   a.part_o = reinterpret_cast<float *>(ws + p.part_o);
   a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
   a.weights = track ? cache->weights : nullptr;
   a.decay = weight_decay;
-  const int nt = attend8_nt(static_cast<int>(std::min<int64_t>(static_cast<int64_t>(tokens) * a.G, 64)));
+  const int nt = attend8_nt(mem->dtype, static_cast<int64_t>(tokens) * a.G);
   return dispatch8(mem, cache->format, [&](auto t, auto d, auto f) {
     using T = decltype(t);
-    if (sizeof(T) == 4 || nt == 1) return launch_attend8<T, d.value, f.value, 1>(a, p, cache->batch, st);
-    if constexpr (sizeof(T) == 2) {
-      if (nt == 2) return launch_attend8<T, d.value, f.value, 2>(a, p, cache->batch, st);
-      return launch_attend8<T, d.value, f.value, 4>(a, p, cache->batch, st);
-    }
-    return MSA_OK;
+    if (nt == 1) return launch_attend8<T, d.value, f.value, 1>(a, p, cache->batch, st);
+    if constexpr (sizeof(T) == 2)
+      if (nt == 4) return launch_attend8<T, d.value, f.value, 4>(a, p, cache->batch, st);
+    return launch_attend8<T, d.value, f.value, 2>(a, p, cache->batch, st);
   });
 }
 
