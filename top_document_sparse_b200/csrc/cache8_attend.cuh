@@ -68,6 +68,8 @@ struct Attend8Args {
   float *lse;
   float2 *ml;        // with weights: reference (log2 units) and 1 / sum of every column's softmax
   float *part_o, *part_ml;
+  float *scores;     // with weights and few columns: [batch][H_kv][cap][score_w] log2-unit scores
+  int score_w;       // 4 or 8
   float *weights;
   float decay;
 };
@@ -555,6 +557,11 @@ cache8_attend_kernel(Attend8Args a) {
         for (int e = 0; e < 4; ++e)
           if (x0 + lg + 8 * (e >> 1) >= rows[nt][e & 1]) s[nt][e] = -INFINITY;
     }
+    if (NT == 1 && a.scores && 2 * lt < a.score_w) {
+      float *out = a.scores + (bh * a.cap + x0 + lg) * a.score_w + 2 * lt;
+      *reinterpret_cast<float2 *>(out) = make_float2(s[0][0], s[0][1]);
+      *reinterpret_cast<float2 *>(out + 8 * a.score_w) = make_float2(s[0][2], s[0][3]);
+    }
     st.step(s);
     st.raise_unit(v_scale);
     const float ratio = v_scale * st.inv_unit;
@@ -886,10 +893,48 @@ cache8_combine_kernel(Attend8Args a, int rows) {
 }
 
 // ---------------------------------------------------------------- weights
-// The weight each cached row received: with the softmax's reference m and sum L known, a second pass
-// over K alone recomputes the scores, p = 2^(s - m) / L, and sums them over the columns, 8 NT at a time with
-// Q's fragments in registers.  Few columns (one round of 8 NT): bound by K's bytes; a warp streams
-// its tiles through a ring.  More: a CTA copies kC8wRows rows to shared memory once and walks over
+// The weight each cached row received, p = 2^(s - m) / L summed over the columns, once the
+// softmax's reference m and sum L are known.
+//   Up to 8 columns: the attention left the scores behind, 16 or 32 bytes a row, and a thread a row
+// adds its weights up (64 queries of up to 8,192 rows, 4 heads a group: 153 us with the attention,
+// 193 with K read a second time).  grid (ceil(cap / 256), B * H_kv), block 256.
+template <int W>
+__global__ void __launch_bounds__(256)
+cache8_weight_scores_kernel(Attend8Args a) {
+  __shared__ float2 stats[W];
+  griddep_wait();
+  griddep_launch();
+  const int b = blockIdx.y / a.H_kv, g = blockIdx.y % a.H_kv;
+  const Attend8Query q = attend8_query(a, b, false);
+  if (static_cast<int>(blockIdx.x) * 256 >= q.len) return;
+  const int cols = q.n * a.G;
+  if (threadIdx.x < W) {
+    const int c = threadIdx.x, t = col_token(a, c);
+    stats[c] = c < cols ? a.ml[(static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + c - t * a.G]
+                        : make_float2(INFINITY, 0.0f);
+  }
+  __syncthreads();
+  const int x = blockIdx.x * 256 + threadIdx.x;
+  if (x >= q.len) return;
+  const int64_t row = (static_cast<int64_t>(b) * a.H_kv + g) * a.cap + x;
+  float sum = 0.0f;
+  if (cols > 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const float4 s = *reinterpret_cast<const float4 *>(a.scores + row * W + i);
+      const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < cols) sum = fmaf(ex2_approx(v[e] - stats[i + e].x), stats[i + e].y, sum);
+    }
+  }
+  float *w = a.weights + row;
+  *w = a.decay == 0.0f ? sum : a.decay * *w + sum;
+}
+
+//   More columns: a second pass
+// over K alone recomputes the scores, 8 NT columns at a time with Q's fragments in registers.  One
+// round of 8 NT: bound by K's bytes; a warp streams its tiles through a ring.  More: a CTA copies kC8wRows rows to shared memory once and walks over
 // all columns, its tiles' sums in registers.
 // grid (CTAs a head, B * H_kv), block 32 * kC8Warps.
 constexpr int kC8wTiles = 4;                              // 16-row tiles a warp, or its ring

@@ -237,7 +237,8 @@ int attend8_nt(msa_dtype t, int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ||
 struct Attend8Plan {
   int n_split = 1, loc_split = 1, col_tiles = 1, table_cap = 0;
   bool tc = false;  // tcgen05: col_tiles is then the number of tile pairs
-  size_t part_o = 0, part_ml = 0, ml = 0, bytes = 0;
+  size_t part_o = 0, part_ml = 0, ml = 0, scores = 0, bytes = 0;
+  int score_w = 0;
 };
 
 // Partial results of the splits, and the softmaxes' statistics where weights are tracked.
@@ -247,7 +248,15 @@ void plan_attend8_scratch(Attend8Plan &p, const msa_memory *mem, const msa_cache
     p.bytes = p.part_ml + round256(rows * p.n_split * 2 * 4);
   }
   p.ml = p.bytes;
-  if (c->weights) p.bytes += round256(rows * 8);
+  if (c->weights) {
+    p.bytes += round256(rows * 8);
+    const size_t cols = rows / c->batch / mem->H_kv;
+    if (cols <= 8) {
+      p.score_w = cols <= 4 ? 4 : 8;
+      p.scores = p.bytes;
+      p.bytes += round256(static_cast<size_t>(c->batch) * mem->H_kv * c->capacity * p.score_w * 4);
+    }
+  }
 }
 
 // Columns (tokens * heads of a group) from which the tcgen05 kernel takes over.  It widens every
@@ -368,7 +377,11 @@ msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B
                         dim3(128), 0, st, a, rows));
     MSA_LAUNCHED("cache8_combine_kernel");
   }
-  if (a.weights) {
+  if (a.scores) {
+    auto sk = p.score_w == 4 ? msa::cache8_weight_scores_kernel<4> : msa::cache8_weight_scores_kernel<8>;
+    MSA_CUDA(launch_pdl(sk, dim3((a.cap + 255) / 256, B * a.H_kv), dim3(256), 0, st, a));
+    MSA_LAUNCHED("cache8_weight_scores_kernel");
+  } else if (a.weights) {
     auto wk = msa::cache8_weight_kernel<T, D, NT, FMT>;
     const int ws = msa::Weight8Smem<D, NT>::kBytes;
     MSA_CUDA(allow_smem(wk, ws));
@@ -445,6 +458,8 @@ msa_status msa_host::cache8_attend(const msa_memory *mem, const void *content, c
   a.loc_split = p.loc_split;
   a.O = O;
   a.lse = lse;
+  a.scores = track && p.score_w ? reinterpret_cast<float *>(ws + p.scores) : nullptr;
+  a.score_w = p.score_w;
   a.ml = track ? reinterpret_cast<float2 *>(ws + p.ml) : nullptr;
   a.part_o = reinterpret_cast<float *>(ws + p.part_o);
   a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
