@@ -60,11 +60,12 @@ template <> struct Fmt8<MSA_CACHE_E4M3> {
 template <int FMT>
 __device__ __forceinline__ float block_scale(float amax) {
   if (amax == 0.0f) return 0.0f;
-  int e;
-  const float m = frexpf(amax, &e);  // amax = m 2^e, m in [0.5, 1)
-  constexpr int eq = FMT == MSA_CACHE_INT8 ? 7 : 9;
-  constexpr float mq = Fmt8<FMT>::kMax / static_cast<float>(1 << eq);  // kMax = mq 2^eq
-  return ldexpf(1.0f, max(e - eq + (m > mq ? 1 : 0), -126));
+  // amax = 1.m 2^e and kMax = 1.n 2^q: the exponent e - q, one more where m > n
+  constexpr int q = FMT == MSA_CACHE_INT8 ? 6 : 8, n = FMT == MSA_CACHE_INT8 ? 0x7e0000 : 0x600000;
+  static_assert(Fmt8<FMT>::kMax == (1.0f + n / 8388608.0f) * (1 << q), "the format's largest value");
+  const int bits = __float_as_int(amax);
+  const int e = max((bits >> 23) - q + ((bits & 0x7fffff) > n ? 1 : 0), 1);  // biased
+  return __int_as_float(e << 23);
 }
 
 // What is stored of a value: NaN as 0, an infinity as the block's largest value.
@@ -200,7 +201,7 @@ __device__ __forceinline__ int append_end(const AppendRange &r, int cap) {
 struct AppendArgs {
   const void *K, *V;
   int64_t kb, kt, vb, vt;  // batch and token strides, elements
-  int tokens, H_kv, cap, bl;
+  int tokens, H_kv, cap, bl, bl_shift;
   uint8_t *k8, *v8;
   float *ks, *vs;
   int32_t *cache_len;
@@ -230,7 +231,7 @@ cache8_append_kernel(AppendArgs a, int set_len) {
   if (!append_range(a.start, a.cache_len, a.n_tokens, b, a.tokens, a.cap, first, r)) return;
   const int end = append_end(r, a.cap);
   if (first && set_len) a.cache_len[b] = end;
-  const int blk = r.start / a.bl + blockIdx.y;
+  const int blk = (r.start >> a.bl_shift) + blockIdx.y;
   const int x0 = blk * a.bl;  // first row of the block
   if (x0 >= end) return;
   const int lo = max(x0, r.start), hi = on ? min(x0 + a.bl, end) : lo;  // new rows [lo, hi)
@@ -239,7 +240,7 @@ cache8_append_kernel(AppendArgs a, int set_len) {
   const int64_t ts = which ? a.vt : a.kt;
   const int64_t bh = static_cast<int64_t>(b) * a.H_kv + h;
   uint8_t *dst = (which ? a.v8 : a.k8) + (bh * a.cap + x0) * D;
-  float *scale = (which ? a.vs : a.ks) + bh * (a.cap / a.bl) + blk;
+  float *scale = (which ? a.vs : a.ks) + bh * (a.cap >> a.bl_shift) + blk;
   Raw16<T> v[NT];
   uint32_t top = 0;
 #pragma unroll
@@ -315,28 +316,28 @@ __global__ void cache8_advance_kernel(int32_t *__restrict__ cache_len,
 }
 
 // ---------------------------------------------------------------- read
-// grid (ceil(rows * H_kv * D / 16 / 256), 2, B): 16 elements a thread, token-major out.
+// grid (ceil(rows * H_kv * D / 16 / 256), 2, B): 16 elements a thread, token-major out.  Bound by the
+// bytes, two thirds of them written.
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(256)
 cache8_read_kernel(const uint8_t *__restrict__ k8, const uint8_t *__restrict__ v8,
                    const float *__restrict__ ks, const float *__restrict__ vs,
                    const int32_t *__restrict__ cache_len, const int32_t *__restrict__ begin,
-                   int rows, int H_kv, int cap, int bl, T *__restrict__ K, T *__restrict__ V) {
+                   int rows, int H_kv, int cap, int bl_shift, T *__restrict__ K, T *__restrict__ V) {
   constexpr int CPR = D / 16;
   griddep_wait();
   griddep_launch();
   const int b = blockIdx.z;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(rows) * H_kv * CPR) return;
-  const int c = static_cast<int>(i % CPR), h = static_cast<int>(i / CPR % H_kv);
-  const int x = static_cast<int>(i / CPR / H_kv);
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;  // (the host keeps the pieces of a query below 2^31)
+  if (i >= static_cast<uint32_t>(rows) * H_kv * CPR) return;
+  const int c = i % CPR, x = i / CPR / static_cast<uint32_t>(H_kv), h = i / CPR - x * H_kv;
   const int64_t row = static_cast<int64_t>(begin ? begin[b] : 0) + x;
   const int len = min(cache_len[b], cap);
   float v[16];
   if (row >= 0 && row < len) {
     const int64_t bh = static_cast<int64_t>(b) * H_kv + h;
     const uint8_t *src = (blockIdx.y ? v8 : k8) + (bh * cap + row) * D + c * 16;
-    const float s = (blockIdx.y ? vs : ks)[bh * (cap / bl) + row / bl];
+    const float s = (blockIdx.y ? vs : ks)[bh * (cap >> bl_shift) + (row >> bl_shift)];
     unpack16<FMT>(*reinterpret_cast<const uint4 *>(src), s, v);
   } else {
 #pragma unroll
@@ -509,7 +510,7 @@ struct EvictMove {
 // wave before it stores it, so in place (one part) needs no synchronisation at all: a wave's
 // stores reach only blocks at or below sources that the same thread has loaded.  Into another
 // cache the kept blocks are split over `parts`.
-constexpr int kMoveWave = 16;
+constexpr int kMoveWave = 8;
 __global__ void __launch_bounds__(128)
 cache8_move_kernel(EvictMove m, const int32_t *__restrict__ src_block,
                    const int32_t *__restrict__ lens, int in_place) {

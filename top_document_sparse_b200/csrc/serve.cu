@@ -178,6 +178,10 @@ msa_status cache8_check(const msa_memory *mem, const msa_cache8 *c) {
   return MSA_OK;
 }
 
+int block_shift(const msa_cache8 *c) {
+  return c->block_len == 16 ? 4 : c->block_len == 32 ? 5 : c->block_len == 64 ? 6 : 7;
+}
+
 template <typename T, int D, int FMT>
 msa_status launch_append(const msa::AppendArgs &a, int B, bool set_len, cudaStream_t st) {
   const int tasks = a.bl * D / 16;
@@ -205,13 +209,13 @@ template <typename T, int D, int FMT>
 msa_status launch_read(const msa_cache8 *c, const int32_t *begin, int rows, int H_kv, void *K,
                        void *V, cudaStream_t st) {
   const int64_t n = (static_cast<int64_t>(rows) * H_kv * (D / 16) + 255) / 256;
-  if (n > 0x7FFFFFFF) return fail(MSA_ERR_UNSUPPORTED, "too many rows");
+  if (n > 0x7FFFFF) return fail(MSA_ERR_UNSUPPORTED, "too many rows for one read");
   MSA_CUDA(launch_pdl(msa::cache8_read_kernel<T, D, FMT>, dim3(static_cast<unsigned>(n), 2, c->batch),
                       dim3(256), 0, st, static_cast<const uint8_t *>(c->k),
                       static_cast<const uint8_t *>(c->v), static_cast<const float *>(c->k_scale),
                       static_cast<const float *>(c->v_scale),
                       static_cast<const int32_t *>(c->cache_len), begin, rows, H_kv, c->capacity,
-                      c->block_len, static_cast<T *>(K), static_cast<T *>(V)));
+                      block_shift(c), static_cast<T *>(K), static_cast<T *>(V)));
   MSA_LAUNCHED("cache8_read_kernel");
   return MSA_OK;
 }
@@ -451,7 +455,7 @@ msa_status msa_host::cache8_attend(const msa_memory *mem, const void *content, c
   a.T = tokens;
   a.cap = cache->capacity;
   a.bl = cache->block_len;
-  a.bl_shift = cache->block_len == 16 ? 4 : cache->block_len == 32 ? 5 : cache->block_len == 64 ? 6 : 7;
+  a.bl_shift = block_shift(cache);
   a.Q = Q;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(mem->D)));
   a.n_split = p.n_split;
@@ -594,6 +598,7 @@ msa_status msa_cache8_append(const msa_memory *mem, const msa_cache8 *cache, con
   a.H_kv = mem->H_kv;
   a.cap = cache->capacity;
   a.bl = cache->block_len;
+  a.bl_shift = block_shift(cache);
   a.k8 = static_cast<uint8_t *>(cache->k);
   a.v8 = static_cast<uint8_t *>(cache->v);
   a.ks = cache->k_scale;
