@@ -13,6 +13,7 @@
 #include "cache8.cuh"
 #include "cache8_attend.cuh"
 #include "cache8_prefill_tc.cuh"
+#include "cache8_weight_tc.cuh"
 #include "rope.cuh"
 
 using namespace msa_host;
@@ -241,9 +242,15 @@ int attend8_nt(msa_dtype t, int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ||
 struct Attend8Plan {
   int n_split = 1, loc_split = 1, col_tiles = 1, table_cap = 0;
   bool tc = false;  // tcgen05: col_tiles is then the number of tile pairs
-  size_t part_o = 0, part_ml = 0, ml = 0, scores = 0, bytes = 0;
+  size_t part_o = 0, part_ml = 0, ml = 0, scores = 0, q16 = 0, factor = 0, bytes = 0;
   int score_w = 0;
+  bool weight_tc = false;
 };
+
+// Columns from which the weights' second pass runs on tcgen05, which takes tiles of 128 of them.
+// tcgen05 against mma.sync: at 96 columns 14 against 21 us for one shape of 8,192 rows and 89 against
+// 97 us for 16 of 4,096; at 48 columns 14 against 16 us and 88 against 66 us.
+constexpr int64_t kWeightTcCols = 96;
 
 // Partial results of the splits, and the softmaxes' statistics where weights are tracked.
 void plan_attend8_scratch(Attend8Plan &p, const msa_memory *mem, const msa_cache8 *c, size_t rows) {
@@ -259,6 +266,12 @@ void plan_attend8_scratch(Attend8Plan &p, const msa_memory *mem, const msa_cache
       p.score_w = cols <= 4 ? 4 : 8;
       p.scores = p.bytes;
       p.bytes += round256(static_cast<size_t>(c->batch) * mem->H_kv * c->capacity * p.score_w * 4);
+    }
+    p.weight_tc = mem->dtype == MSA_BF16 && mem->D == 128 && static_cast<int64_t>(cols) >= kWeightTcCols;
+    if (p.weight_tc) {
+      p.q16 = p.bytes;
+      p.factor = p.q16 + round256(rows * mem->D * 2);
+      p.bytes = p.factor + round256(rows * 4);
     }
   }
 }
@@ -352,7 +365,8 @@ msa_status launch_prefill8(const msa::Attend8Args &a, const Attend8Plan &p, int 
 }
 
 template <typename T, int D, int FMT, int NT>
-msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B, cudaStream_t st) {
+msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B, uint8_t *ws,
+                          cudaStream_t st) {
   constexpr bool kBf16 = sizeof(T) == 2;
   const dim3 block(32 * msa::kC8Warps);
   const int own = p.n_split - p.loc_split;
@@ -385,16 +399,29 @@ msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B
     auto sk = p.score_w == 4 ? msa::cache8_weight_scores_kernel<4> : msa::cache8_weight_scores_kernel<8>;
     MSA_CUDA(launch_pdl(sk, dim3((a.cap + 255) / 256, B * a.H_kv), dim3(256), 0, st, a));
     MSA_LAUNCHED("cache8_weight_scores_kernel");
+  } else if (kBf16 && D == 128 && a.weights && p.weight_tc) {
+    auto wk = msa::cache8_weight_tc_kernel<FMT>;
+    auto *q16 = reinterpret_cast<__half *>(ws + p.q16);
+    auto *factor = reinterpret_cast<float *>(ws + p.factor);
+    const int64_t cols = static_cast<int64_t>(B) * a.T * a.H_kv * a.G;
+    MSA_CUDA(launch_pdl(msa::cache8_q16_kernel, dim3(static_cast<unsigned>((cols + 7) / 8)), dim3(256), 0,
+                        st, a, B, q16, factor));
+    MSA_LAUNCHED("cache8_q16_kernel");
+    MSA_CUDA(allow_smem(wk, msa::CwSmem::kBytes));
+    MSA_CUDA(launch_pdl(wk, dim3((a.cap + msa::kCwRows - 1) / msa::kCwRows, B * a.H_kv),
+                        dim3(msa::kCwThreads), msa::CwSmem::kBytes, st, a,
+                        static_cast<const __half *>(q16), static_cast<const float *>(factor)));
+    MSA_LAUNCHED("cache8_weight_tc_kernel");
   } else if (a.weights) {
     auto wk = msa::cache8_weight_kernel<T, D, NT, FMT>;
-    const int ws = msa::Weight8Smem<D, NT>::kBytes;
-    MSA_CUDA(allow_smem(wk, ws));
+    const int smem = msa::Weight8Smem<D, NT>::kBytes;
+    MSA_CUDA(allow_smem(wk, smem));
     // one round of columns: a CTA streams its share of the tiles, about eight CTAs an SM in all
     // (a CTA's set-up takes as long as a dozen tiles); more rounds: a CTA for every kC8wRows rows
     const int chunks = (a.cap + msa::kC8wRows - 1) / msa::kC8wRows;
     const bool stream = static_cast<int64_t>(a.T) * a.G <= 8 * NT;
     const int grid_x = stream ? std::min(chunks, (8 * num_sms() + B * a.H_kv - 1) / (B * a.H_kv)) : chunks;
-    MSA_CUDA(launch_pdl(wk, dim3(grid_x, B * a.H_kv), block, ws, st, a, stream ? 1 : 0));
+    MSA_CUDA(launch_pdl(wk, dim3(grid_x, B * a.H_kv), block, smem, st, a, stream ? 1 : 0));
     MSA_LAUNCHED("cache8_weight_kernel");
   }
   return MSA_OK;
@@ -472,10 +499,10 @@ msa_status msa_host::cache8_attend(const msa_memory *mem, const void *content, c
   const int nt = attend8_nt(mem->dtype, static_cast<int64_t>(tokens) * a.G);
   return dispatch8(mem, cache->format, [&](auto t, auto d, auto f) {
     using T = decltype(t);
-    if (nt == 1) return launch_attend8<T, d.value, f.value, 1>(a, p, cache->batch, st);
+    if (nt == 1) return launch_attend8<T, d.value, f.value, 1>(a, p, cache->batch, ws, st);
     if constexpr (sizeof(T) == 2)
-      if (nt == 4) return launch_attend8<T, d.value, f.value, 4>(a, p, cache->batch, st);
-    return launch_attend8<T, d.value, f.value, 2>(a, p, cache->batch, st);
+      if (nt == 4) return launch_attend8<T, d.value, f.value, 4>(a, p, cache->batch, ws, st);
+    return launch_attend8<T, d.value, f.value, 2>(a, p, cache->batch, ws, st);
   });
 }
 
