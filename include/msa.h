@@ -628,7 +628,9 @@ MSA_API msa_status msa_cache8_read(const msa_memory *mem, const msa_cache8 *cach
                                    const int32_t *begin, int32_t rows, void *K_out, void *V_out,
                                    msa_stream stream);
 
-/* Scratch bytes msa_cache8_attend needs. */
+/* Scratch bytes msa_cache8_attend needs.  A cache with weights needs up to 64 a
+ * cached row and kv head where a kv head has at most 16 columns (tokens * heads
+ * of the group): the scores are kept for the weights. */
 MSA_API size_t msa_cache8_attend_workspace_size(const msa_memory *mem, const msa_cache8 *cache,
                                                 int32_t tokens, int32_t k, int32_t n_q_heads);
 

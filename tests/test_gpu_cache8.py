@@ -250,7 +250,8 @@ def test_attend_matches_fp64(case):
 @pytest.mark.parametrize("dt,fmt,T,G,decay", [("bf16", "int8", 1, 4, 0.0), ("bf16", "e4m3", 7, 3, 1.0),
                                               ("f32", "int8", 2, 2, 0.5), ("bf16", "int8", 40, 2, 0.9),
                                               ("bf16", "e4m3", 30, 3, 0.25),
-                                              ("bf16", "int8", 100, 4, 1.0), ("bf16", "e4m3", 50, 3, 0.5)])
+                                              ("bf16", "int8", 100, 4, 1.0), ("bf16", "e4m3", 50, 3, 0.5),
+                                              ("bf16", "int8", 3, 4, 0.7), ("f32", "e4m3", 8, 2, 0.0)])
 def test_attend_accumulates_weights(dt, fmt, T, G, decay):
     D = 128 if T in (30, 50, 100) else 64
     mem, content = memory(torch.bfloat16 if dt == "bf16" else torch.float32, 2, D)

@@ -69,7 +69,7 @@ struct Attend8Args {
   float2 *ml;        // with weights: reference (log2 units) and 1 / sum of every column's softmax
   float *part_o, *part_ml;
   float *scores;     // with weights and few columns: [batch][H_kv][cap][score_w] log2-unit scores
-  int score_w;       // 4 or 8
+  int score_w;       // 4, 8 or 16
   float *weights;
   float decay;
 };
@@ -557,10 +557,14 @@ cache8_attend_kernel(Attend8Args a) {
         for (int e = 0; e < 4; ++e)
           if (x0 + lg + 8 * (e >> 1) >= rows[nt][e & 1]) s[nt][e] = -INFINITY;
     }
-    if (NT == 1 && a.scores && 2 * lt < a.score_w) {
+    if (NT <= 2 && a.scores) {
       float *out = a.scores + (bh * a.cap + x0 + lg) * a.score_w + 2 * lt;
-      *reinterpret_cast<float2 *>(out) = make_float2(s[0][0], s[0][1]);
-      *reinterpret_cast<float2 *>(out + 8 * a.score_w) = make_float2(s[0][2], s[0][3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (NT == 2 || 2 * lt < a.score_w) {
+          *reinterpret_cast<float2 *>(out + 8 * nt) = make_float2(s[nt][0], s[nt][1]);
+          *reinterpret_cast<float2 *>(out + 8 * a.score_w + 8 * nt) = make_float2(s[nt][2], s[nt][3]);
+        }
     }
     st.step(s);
     st.raise_unit(v_scale);
@@ -826,21 +830,28 @@ cache8_memory_f32_kernel(Attend8Args a) {
 }
 
 // ---------------------------------------------------------------- combine
-// grid ceil(rows / 4), block 128: merge the context splits (at most kC8MaxSplit), a warp a row of
-// O (token, head), a lane D / 32 elements.
+// Merge the context splits (at most kC8MaxSplit) of a row of O (token, head): W warps a row, each a
+// W-th of its splits, a lane D / 32 elements.  One warp sums many splits in rounds of eight loads, a
+// latency each; four overlap them (the whole call, 4 warps against 1: one query of 8 splits 7.9
+// against 8.9 us, 4 tokens over 32,768 rows in 27 splits 26.3 against 28.3; 5 splits of 2,048 rows
+// of O the same).
+// grid ceil(rows * W / 4), block 128.
 constexpr int kC8MaxSplit = 128;
-template <typename T, int D>
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(128)
 cache8_combine_kernel(Attend8Args a, int rows) {
   constexpr int E = D / 32;
+  using Vec = std::conditional_t<E == 4, float4, float2>;
+  __shared__ Vec parts[W == 1 ? 1 : W - 1][32];
   griddep_wait();
   griddep_launch();
-  const int row = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int row = W == 1 ? blockIdx.x * 4 + warp : blockIdx.x, w = W == 1 ? 0 : warp;
   if (row >= rows) return;
   const int H_q = a.H_kv * a.G;
   const int b = row / H_q / a.T, t = row / H_q % a.T;
   const Attend8Query q = attend8_query(a, b, false);
-  if (t >= q.n) return;
+  if (t >= q.n) return;  // (W == 4: the whole block)
   const int n = a.n_split;
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + static_cast<int64_t>(row) * n;
   const float *part = a.part_o + static_cast<int64_t>(row) * n * D + lane * E;
@@ -853,7 +864,8 @@ cache8_combine_kernel(Attend8Args a, int rows) {
   }
   M = warp_max(M);
   const float base = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f, o[E];
+  float L = 0.0f;
+  __align__(16) float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
 #pragma unroll
@@ -863,20 +875,23 @@ cache8_combine_kernel(Attend8Args a, int rows) {
     L += x[i].y * f;
     const int m = min(32, n - 32 * i);
 #pragma unroll 8
-    for (int s = 0; s < m; ++s) {
+    for (int s = w; s < m; s += W) {
       const float fs = __shfl_sync(0xffffffffu, f, s);
-      const float *p = part + static_cast<int64_t>(32 * i + s) * D;
-      if constexpr (E == 4) {
-        const float4 y = *reinterpret_cast<const float4 *>(p);
-        o[0] = fmaf(y.x, fs, o[0]);
-        o[1] = fmaf(y.y, fs, o[1]);
-        o[2] = fmaf(y.z, fs, o[2]);
-        o[3] = fmaf(y.w, fs, o[3]);
-      } else {
-        const float2 y = *reinterpret_cast<const float2 *>(p);
-        o[0] = fmaf(y.x, fs, o[0]);
-        o[1] = fmaf(y.y, fs, o[1]);
-      }
+      const Vec y = *reinterpret_cast<const Vec *>(part + static_cast<int64_t>(32 * i + s) * D);
+      const float *v = reinterpret_cast<const float *>(&y);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(v[e], fs, o[e]);
+    }
+  }
+  if constexpr (W > 1) {
+    if (w > 0) parts[w - 1][lane] = *reinterpret_cast<const Vec *>(o);
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int u = 0; u < W - 1; ++u) {
+      const Vec y = parts[u][lane];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += reinterpret_cast<const float *>(&y)[e];
     }
   }
   L = warp_sum(L);
@@ -895,9 +910,10 @@ cache8_combine_kernel(Attend8Args a, int rows) {
 // ---------------------------------------------------------------- weights
 // The weight each cached row received, p = 2^(s - m) / L summed over the columns, once the
 // softmax's reference m and sum L are known.
-//   Up to 8 columns: the attention left the scores behind, 16 or 32 bytes a row, and a thread a row
-// adds its weights up (64 queries of up to 8,192 rows, 4 heads a group: 153 us with the attention,
-// 193 with K read a second time).  grid (ceil(cap / 256), B * H_kv), block 256.
+//   Up to 16 columns: the attention left the scores behind, 16, 32 or 64 bytes a row, and a thread a
+// row adds its weights up.  With the attention, against K read a second time: 64 queries of up to
+// 8,192 rows, 4 columns, 153 against 193 us; 16 columns of 2 x 32,768 rows 52 against 56 (e4m3) or 53
+// against 60 (int8), of 16 x 4,096 rows 59 against 71.  grid (ceil(cap / 256), B * H_kv), block 256.
 template <int W>
 __global__ void __launch_bounds__(256)
 cache8_weight_scores_kernel(Attend8Args a) {
@@ -932,10 +948,10 @@ cache8_weight_scores_kernel(Attend8Args a) {
   *w = a.decay == 0.0f ? sum : a.decay * *w + sum;
 }
 
-//   More columns: a second pass
-// over K alone recomputes the scores, 8 NT columns at a time with Q's fragments in registers.  One
-// round of 8 NT: bound by K's bytes; a warp streams its tiles through a ring.  More: a CTA copies kC8wRows rows to shared memory once and walks over
-// all columns, its tiles' sums in registers.
+//   More columns: a second pass over K alone recomputes the scores, 8 NT columns at a time with Q's
+// fragments in registers.  One round of 8 NT: bound by K's bytes; a warp streams its tiles through a
+// ring.  More: a CTA copies kC8wRows rows to shared memory once and walks over all columns, its
+// tiles' sums in registers.
 // grid (CTAs a head, B * H_kv), block 32 * kC8Warps.
 constexpr int kC8wTiles = 4;                              // 16-row tiles a warp, or its ring
 constexpr int kC8wRows = 16 * kC8wTiles * kC8Warps;

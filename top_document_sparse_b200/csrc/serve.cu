@@ -262,8 +262,8 @@ void plan_attend8_scratch(Attend8Plan &p, const msa_memory *mem, const msa_cache
   if (c->weights) {
     p.bytes += round256(rows * 8);
     const size_t cols = rows / c->batch / mem->H_kv;
-    if (cols <= 8) {
-      p.score_w = cols <= 4 ? 4 : 8;
+    if (cols <= 16) {
+      p.score_w = cols <= 4 ? 4 : cols <= 8 ? 8 : 16;
       p.scores = p.bytes;
       p.bytes += round256(static_cast<size_t>(c->batch) * mem->H_kv * c->capacity * p.score_w * 4);
     }
@@ -391,12 +391,16 @@ msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B
   }
   if (p.n_split > 1) {
     const int rows = B * a.T * a.H_kv * a.G;
-    MSA_CUDA(launch_pdl(msa::cache8_combine_kernel<T, D>, dim3((static_cast<unsigned>(rows) + 3) / 4),
-                        dim3(128), 0, st, a, rows));
+    const bool many = p.n_split > 4;
+    auto ck = many ? msa::cache8_combine_kernel<T, D, 4> : msa::cache8_combine_kernel<T, D, 1>;
+    const unsigned grid = many ? rows : (static_cast<unsigned>(rows) + 3) / 4;
+    MSA_CUDA(launch_pdl(ck, dim3(grid), dim3(128), 0, st, a, rows));
     MSA_LAUNCHED("cache8_combine_kernel");
   }
   if (a.scores) {
-    auto sk = p.score_w == 4 ? msa::cache8_weight_scores_kernel<4> : msa::cache8_weight_scores_kernel<8>;
+    auto sk = p.score_w == 4   ? msa::cache8_weight_scores_kernel<4>
+              : p.score_w == 8 ? msa::cache8_weight_scores_kernel<8>
+                               : msa::cache8_weight_scores_kernel<16>;
     MSA_CUDA(launch_pdl(sk, dim3((a.cap + 255) / 256, B * a.H_kv), dim3(256), 0, st, a));
     MSA_LAUNCHED("cache8_weight_scores_kernel");
   } else if (kBf16 && D == 128 && a.weights && p.weight_tc) {
@@ -412,7 +416,8 @@ msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B
                         dim3(msa::kCwThreads), msa::CwSmem::kBytes, st, a,
                         static_cast<const __half *>(q16), static_cast<const float *>(factor)));
     MSA_LAUNCHED("cache8_weight_tc_kernel");
-  } else if (a.weights) {
+  } else if constexpr (NT == (kBf16 ? 4 : 2)) {  // (fewer columns left their scores behind)
+    if (!a.weights) return MSA_OK;
     auto wk = msa::cache8_weight_kernel<T, D, NT, FMT>;
     const int smem = msa::Weight8Smem<D, NT>::kBytes;
     MSA_CUDA(allow_smem(wk, smem));
