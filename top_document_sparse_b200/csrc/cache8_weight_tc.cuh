@@ -240,12 +240,12 @@ cache8_weight_tc_kernel(Attend8Args a, const __half *__restrict__ q16, const flo
           const float4 cf = *reinterpret_cast<const float4 *>(c + h + i);
           const float4 nm = *reinterpret_cast<const float4 *>(c + kCwCols + h + i);
           const float4 il = *reinterpret_cast<const float4 *>(c + 2 * kCwCols + h + i);
-          // (ks is a power of two, so the products round as the attention's did)
+          // factors first: they round and overflow only where the attention's did
           const float2 k2 = make_float2(ks, ks);
-          float2 e0 = mul2(mul2(make_float2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), k2),
-                           make_float2(cf.x, cf.y));
-          float2 e1 = mul2(mul2(make_float2(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3])), k2),
-                           make_float2(cf.z, cf.w));
+          float2 e0 = mul2(mul2(make_float2(cf.x, cf.y), k2),
+                           make_float2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])));
+          float2 e1 = mul2(mul2(make_float2(cf.z, cf.w), k2),
+                           make_float2(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3])));
           e0 = add2(e0, make_float2(nm.x, nm.y));
           e1 = add2(e1, make_float2(nm.z, nm.w));
           float2 p0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
