@@ -144,3 +144,25 @@ def test_rope_refuses():
                 lambda: rope.rotate(q, None, pos.cpu()), lambda: rope.rotate(q.half(), None, pos)):
         with pytest.raises((ValueError, TypeError)):
             bad()
+
+
+def test_rope_on_another_stream_leaves_freed_blocks_alone():
+    """A block that the current stream freed while work there still reads it must not become the
+    output of a call on another stream."""
+    from top_document_sparse_b200 import msa
+    rope = msa.Rope(64)
+    n = 5000
+    q = torch.randn(n, 8, 64, device="cuda")
+    pos = torch.arange(n, device="cuda")
+    other = torch.cuda.Stream()
+    keep = torch.empty_like(q)
+    torch.cuda.synchronize()
+    want, _ = rope.rotate(q, None, pos)
+    torch.cuda.synchronize()
+    freed = torch.full_like(q, 7.0)
+    torch.cuda._sleep(20_000_000)
+    keep.copy_(freed)
+    del freed  # its block is free for the current stream's next allocation
+    got, _ = rope.rotate(q, None, pos, stream=other)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.all(keep == 7.0)

@@ -505,6 +505,15 @@ def _call(fn, device, stream, *args):
         _check(status)
 
 
+def _output(stream, make, *args, **kw):
+    """An output for a call on `stream`, from that stream's memory: a block that the current stream
+    has freed may still be read by work queued there."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _device(device) -> torch.device:
     d = torch.device(device)
     if d.type != "cuda":
@@ -519,7 +528,8 @@ class Rope:
 
     q and k are [..., heads, head_dim] with the same leading dimensions as ``positions`` (int64),
     fp32 or bf16; heads of a token are dense and tokens evenly spaced, so slices of a joint
-    projection are taken as they lie.  k may be None."""
+    projection are taken as they lie.  k may be None.  Outputs that are not given are allocated on
+    the call's stream."""
 
     LAYOUTS = {"half": 0, "interleaved": 1}
     SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -590,7 +600,7 @@ class Rope:
         dtype = q.dtype
         qp, qh, qs = self._side(q, "q", lead, dtype)
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = _output(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
             qo, qoh, qos = q_out.data_ptr(), qh, qh * self.head_dim
         else:
             qo, qoh, qos = self._side(q_out, "q_out", lead, dtype)
@@ -598,7 +608,7 @@ class Rope:
         if k is not None:
             kp, kh, ks = self._side(k, "k", lead, dtype)
             if k_out is None:
-                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+                k_out = _output(stream, torch.empty_like, k, memory_format=torch.contiguous_format)
                 ko, koh, kos = k_out.data_ptr(), kh, kh * self.head_dim
             else:
                 ko, koh, kos = self._side(k_out, "k_out", lead, dtype)
@@ -682,9 +692,9 @@ class Cache8:
         mem = self.mem
         shape = (self.batch, rows, mem.n_kv_heads, mem.head_dim)
         if K_out is None:
-            K_out = torch.empty(shape, dtype=mem.dtype, device=self.device)
+            K_out = _output(stream, torch.empty, shape, dtype=mem.dtype, device=self.device)
         if V_out is None:
-            V_out = torch.empty_like(K_out)
+            V_out = _output(stream, torch.empty_like, K_out)
         _call(_lib.msa_cache8_read, self.device, stream, mem.handle, self._ref,
               self._counts(begin, "begin"), rows,
               _tensor(K_out, "K_out", shape, mem.dtype, self.device.index),
