@@ -275,6 +275,15 @@ def test_attend_magnitudes(q_scale, spread):
     run_attend(mem, content, cache, ref, ids, 40, 2, None, q_scale=q_scale)
 
 
+@pytest.mark.parametrize("T", [2, 20, 80])  # scores kept, recomputed on mma.sync, on tcgen05
+@pytest.mark.parametrize("q_scale,spread", [(4.0, 0.0), (2.0 ** -90, 3.0), (1.0, 8.0)])
+def test_weights_magnitudes(T, q_scale, spread):
+    mem, content = memory(torch.bfloat16, 1, 128)
+    cache, ref = filled(mem, 2, 512, 16, "int8", [512, 333], seed=4, spread=spread, track=True)
+    ids = torch.tensor([[0, 3], [1, 5]], dtype=torch.int32, device="cuda")
+    run_attend(mem, content, cache, ref, ids, T, 2, None, q_scale=q_scale, decay=0.0)
+
+
 @pytest.mark.parametrize("T", [1, 40])
 @pytest.mark.parametrize("k_scale,v_scale", [(2.0 ** -30, 2.0 ** 40), (8.0, 2.0 ** -40), (0.0, 0.0)])
 def test_attend_memory_magnitudes(T, k_scale, v_scale):
