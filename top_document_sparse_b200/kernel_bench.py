@@ -7,8 +7,10 @@ Stages: ``route`` (msa_route: query normalisation, route score, top-k), ``topk``
 no query rows), ``attend`` (msa_sparse_attend of one token over k retrieved documents plus the
 local cache), ``prefill`` (msa_sparse_attend of the workload's query tokens), and the widening
 calls: ``backward`` (msa_route_backward and msa_sparse_attend_backward of one decode token),
-``merge`` (msa_topk_merge of four shards' candidates) and ``update`` (msa_encode_memory of one
-512-token document).  The router keys are random unit vectors and the pooled content random bf16, so
+``merge`` (msa_topk_merge of four shards' candidates), ``update`` (msa_encode_memory of one
+512-token document) and ``cache8`` (one decode token over the 8-bit local cache: msa_rope_apply,
+msa_cache8_append, msa_cache8_attend without and with the rows' weights, and msa_cache8_evict of a
+quarter of the rows into another cache).  The router keys are random unit vectors and the pooled content random bf16, so
 no encode pass is needed.  Calls are captured in a CUDA graph and timed with CUDA events; each
 call reads more than the 126 MB L2 only for memories of 64K+ chunks, so small workloads report
 L2-warm figures (printed as "l2_warm").  Used for the ncu captures summarised under profiles/.
@@ -46,7 +48,7 @@ def _graph_time(fn, reps):
     return a.elapsed_time(b) / reps * 1e3  # us per call
 
 
-STAGES = ["all", "route", "topk", "attend", "prefill", "backward", "merge", "update"]
+STAGES = ["all", "route", "topk", "attend", "prefill", "backward", "merge", "update", "cache8"]
 
 
 def main(argv=None):
@@ -176,6 +178,35 @@ def run(workload: str, stages, reps: int = 20, seed: int = 0) -> dict:
                 + (ct.numel() + 2 * Kc.numel() + Q.numel()) * 4)
         out["attend_backward_us"] = round(t, 2)
         out["attend_backward_gbs"] = round(byts / (t * 1e-6) / 1e9, 1)
+    if "cache8" in st_set:
+        ct = torch.randn(mem.n_chunks, 2, H_kv, D, device="cuda", generator=gen).to(torch.bfloat16)
+        ids = torch.from_numpy(np.stack([np.random.default_rng(b).choice(mem.n_docs, k, replace=False)
+                                         for b in range(B)]).astype(np.int32)).cuda()
+        L0 = w.query_tokens + max(w.decode_steps, 1) // 2
+        bl = 64
+        cap8 = -(-cap // bl) * bl
+        cache = msa.Cache8(mem, B, cap8, bl, "int8", track_weights=True)
+        small = msa.Cache8(mem, B, cap8, bl, "int8", track_weights=True)
+        kv = torch.randn(2, B, L0, H_kv, D, device="cuda", generator=gen).to(torch.bfloat16)
+        cache.append(kv[0], kv[1])
+        q = torch.randn(B, 1, H_q, D, device="cuda", generator=gen).to(torch.bfloat16)
+        pos = torch.full((B, 1), k + L0, dtype=torch.int64, device="cuda")
+        start = torch.full((B,), L0, dtype=torch.int32, device="cuda")
+        rope = msa.Rope(D, theta=w.rope_theta)
+        qr, kr = torch.empty_like(q), torch.empty_like(kv[0, :, :1])
+        K1, V1, O = kv[0, :, :1].contiguous(), kv[1, :, :1].contiguous(), torch.empty_like(q)
+        ws = msa.workspace(max(cache.attend_workspace_size(1, k, H_q), cache.evict_workspace_size()))
+        calls = {"rope": lambda: rope.rotate(q, K1, pos, q_out=qr, k_out=kr),
+                 "append": lambda: cache.append(kr, V1, start=start),
+                 "attend": lambda: cache.attend(ct, ids, qr, O, ws),
+                 "attend_weights": lambda: cache.attend(ct, ids, qr, O, ws, weight_decay=1.0),
+                 "evict": lambda: cache.evict(L0 * 3 // 4, bl, ws, out=small)}
+        n_mem = int(sum(mem.doc_chunk_offsets[d + 1] - mem.doc_chunk_offsets[d]
+                        for d in ids.cpu().numpy().ravel()))
+        for name, fn in calls.items():
+            out[f"cache8_{name}_us"] = round(_graph_time(fn, reps), 2)
+        byts = n_mem * H_kv * 2 * D * 2 + B * (L0 + 1) * H_kv * 2 * D
+        out["cache8_attend_gbs"] = round(byts / (out["cache8_attend_us"] * 1e-6) / 1e9, 1)
     if "merge" in st_set:
         # Memory Parallel: four shards' top-k candidates merged into the global top-k
         n_sh = 4
