@@ -21,6 +21,7 @@ from cache8_ref import f64
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -23
+BAD_DOC_ID = 0x1
 
 
 def memory(dtype, H, D, docs=(70, 1, 64, 200, 129, 33)):
@@ -284,6 +285,37 @@ def test_weights_magnitudes(T, q_scale, spread):
     run_attend(mem, content, cache, ref, ids, T, 2, None, q_scale=q_scale, decay=0.0)
 
 
+@pytest.mark.parametrize("T,G", [(4, 4), (20, 2), (60, 2)])  # the three paths again
+def test_weights_where_tokens_see_nothing(T, G):
+    mem, content = memory(torch.bfloat16, 1, 128)
+    cache, ref = filled(mem, 3, 320, 32, "e4m3", [2, 300, 0], seed=8, track=True)
+    for i in range(2):  # more new tokens than rows: the first ones see no row, and there is no memory
+        run_attend(mem, content, cache, ref, None, T, G, None, decay=0.5, seed=30 + i)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [1, 40])
+def test_attend_repeated_and_bad_ids(dt, T):
+    """A document named twice counts twice; ids out of range bring no rows and are flagged."""
+    from top_document_sparse_b200 import msa
+    mem, content = memory(dt, 2, 128)
+    cache, ref = filled(mem, 2, 128, 32, "int8", [128, 70], seed=8)
+    twice = torch.tensor([[3, 3, 0], [1, 1, 1]], dtype=torch.int32, device="cuda")
+    run_attend(mem, content, cache, ref, twice, T, 2, None)
+    good = torch.tensor([[2], [5]], dtype=torch.int32, device="cuda")
+    bad = torch.tensor([[-1, 2, 6], [5, 2 ** 31 - 1, -7]], dtype=torch.int32, device="cuda")
+    want, _ = run_attend(mem, content, cache, ref, good, T, 2, None, seed=12)
+    Q = (torch.randn(*want.shape, generator=torch.Generator(device="cuda").manual_seed(12), device="cuda")).to(dt)
+    O = torch.empty_like(Q)
+    cache.attend(content, bad, Q, O, msa.workspace(cache.attend_workspace_size(T, 3, 4)))
+    assert msa.device_error() == BAD_DOC_ID
+    # each is within the output's rounding, a weight's (2^-11 in bf16, 2^-22 in fp32) and the sums'
+    # (half a weight's; 4,300 rows' in fp32) of the exact value, none larger than the largest V
+    top = max(float(content[:, 1].abs().max()), float(cache.read(None, 128)[1].abs().max()))
+    step = 2.0 ** -8 + 1.5 * 2.0 ** -11 if dt == torch.bfloat16 else 2.0 ** -24 + 1.5 * 2.0 ** -22 + 4300 * U
+    assert float((O.double() - want.double()).abs().max()) <= 2 * step * top
+
+
 @pytest.mark.parametrize("T", [1, 40])
 @pytest.mark.parametrize("k_scale,v_scale", [(2.0 ** -30, 2.0 ** 40), (8.0, 2.0 ** -40), (0.0, 0.0)])
 def test_attend_memory_magnitudes(T, k_scale, v_scale):
@@ -337,7 +369,8 @@ def test_attend_and_append_past_32_bit_offsets():
     cache.append(kv[0], kv[1], start=start)
     Kr, _ = cache.read(start, 2)
     assert torch.all((Kr.float() - kv[0].float()).abs() <= 2.0 ** -6)  # half a step of the largest scale
-    for T, G in ((1, 1), (2, 24 // 2)):
+    # (8 x 12 columns run on tcgen05, which adds 16 rows an accumulation into at most n / 128 partial sums)
+    for T, G, sums in ((1, 1, 0), (2, 24 // 2, 0), (8, 12, (cap - 1) / 128)):
         Q = torch.randn(B, T, H * G, D, generator=g, device="cuda").bfloat16()
         O, lse = torch.empty_like(Q), torch.empty(B, T, H * G, device="cuda")
         cache.attend(None, None, Q, O, msa.workspace(cache.attend_workspace_size(T, 0, H * G)), lse=lse,
@@ -351,7 +384,7 @@ def test_attend_and_append_past_32_bit_offsets():
         want, size = p @ V, p @ V.abs()
         # see the bounds above; the row sum's error grows with the square root of the rows here, but
         # is bounded by (rows / 512) u: a split's lane adds that many terms
-        tol = (2.0 ** -11 + 2.0 ** -12 + n / 512 * U) * size + n * 2.0 ** -28 * 2
+        tol = (2.0 ** -11 + 2.0 ** -12 + (n / 512 + sums) * U) * size + n * 2.0 ** -28 * 2
         err = (O[b, -1, h * G].double() - want).abs()
         assert torch.all(err <= tol + 2.0 ** -8 * (want.abs() + tol))
         assert abs(float(lse[b, -1, h * G]) - float(torch.logsumexp(z, 0))) <= 1e-4
