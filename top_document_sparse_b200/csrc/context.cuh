@@ -71,14 +71,13 @@ __device__ __forceinline__ int build_chunk_table(const int32_t *__restrict__ ids
   return n_mem;
 }
 
-// The chunk table of query b built by one warp (the loader): table[x] = chunk
-// row of context row x < n_mem, ranks in order; the same rows as
-// build_chunk_table.  Returns n_mem in every lane.
-__device__ __forceinline__ int build_chunk_table_warp(const int32_t *__restrict__ ids_b, int k,
-                                                      const int64_t *__restrict__ doc_chunk_off,
-                                                      int n_docs, const int32_t *__restrict__ slots_b,
-                                                      int slot_chunks, int *table, int *pre,
-                                                      int *base, int table_cap, int lane) {
+// One warp's part of the chunk table of query b: pre[0..k] (context rows before each rank) and
+// base[0..k) (each rank's first chunk row).  Returns n_mem in every lane.
+__device__ __forceinline__ int chunk_prefix_warp(const int32_t *__restrict__ ids_b, int k,
+                                                 const int64_t *__restrict__ doc_chunk_off,
+                                                 int n_docs, const int32_t *__restrict__ slots_b,
+                                                 int slot_chunks, int *pre, int *base,
+                                                 int table_cap, int lane) {
   int cnt[2] = {0, 0};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -114,14 +113,30 @@ __device__ __forceinline__ int build_chunk_table_warp(const int32_t *__restrict_
   const int n_mem = min(run, table_cap);
   if (lane == 0) pre[k] = n_mem;
   __syncwarp();
-  for (int x = lane; x < n_mem; x += 32) {
-    int lo = 0, hi = k - 1;  // last rank r with pre[r] <= x
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= x) lo = mid; else hi = mid - 1;
-    }
-    table[x] = base[lo] + (x - pre[lo]);
+  return n_mem;
+}
+
+// Chunk row of context row x < n_mem.
+__device__ __forceinline__ int chunk_row(const int *pre, const int *base, int k, int x) {
+  int lo = 0, hi = k - 1;  // last rank r with pre[r] <= x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid - 1;
   }
+  return base[lo] + (x - pre[lo]);
+}
+
+// The chunk table of query b built by one warp (the loader): table[x] = chunk
+// row of context row x < n_mem, ranks in order; the same rows as
+// build_chunk_table.  Returns n_mem in every lane.
+__device__ __forceinline__ int build_chunk_table_warp(const int32_t *__restrict__ ids_b, int k,
+                                                      const int64_t *__restrict__ doc_chunk_off,
+                                                      int n_docs, const int32_t *__restrict__ slots_b,
+                                                      int slot_chunks, int *table, int *pre,
+                                                      int *base, int table_cap, int lane) {
+  const int n_mem = chunk_prefix_warp(ids_b, k, doc_chunk_off, n_docs, slots_b, slot_chunks, pre, base,
+                                      table_cap, lane);
+  for (int x = lane; x < n_mem; x += 32) table[x] = chunk_row(pre, base, k, x);
   __syncwarp();
   return n_mem;
 }
