@@ -252,14 +252,15 @@ def test_attend_matches_fp64(case):
                                               ("f32", "int8", 2, 2, 0.5), ("bf16", "int8", 40, 2, 0.9),
                                               ("bf16", "e4m3", 30, 3, 0.25),
                                               ("bf16", "int8", 100, 4, 1.0), ("bf16", "e4m3", 50, 3, 0.5),
-                                              ("bf16", "int8", 3, 4, 0.7), ("f32", "e4m3", 8, 2, 0.0)])
+                                              ("bf16", "int8", 3, 4, 0.7), ("f32", "e4m3", 8, 2, 0.0),
+                                              ("bf16", "int8", 51, 4, 0.5), ("bf16", "e4m3", 33, 3, 0.0)])
 def test_attend_accumulates_weights(dt, fmt, T, G, decay):
     D = 128 if T in (30, 50, 100) else 64
     mem, content = memory(torch.bfloat16 if dt == "bf16" else torch.float32, 2, D)
     lens, n = [200, 1, 77, 150], [T, 1, T // 2, T]
-    if T == 100:  # several tiles of rows and of columns
+    if T in (51, 100):  # several tiles of rows and of columns
         lens, n = [700, 1, 77, 257], [T, 1, 50, 0]
-    cache, ref = filled(mem, 4, 256 if T < 100 else 704, 32, fmt, lens, seed=9, track=True)
+    cache, ref = filled(mem, 4, 704 if T in (51, 100) else 256, 32, fmt, lens, seed=9, track=True)
     ids = torch.tensor([[0, 3], [1, 2], [5, 4], [3, 0]], dtype=torch.int32, device="cuda")
     for i in range(3):
         run_attend(mem, content, cache, ref, ids, T, G, n, decay=decay, seed=20 + i)

@@ -17,7 +17,8 @@
 //   warps 0-7    S from TMEM, the weights added up in registers
 // The special-function unit is the floor: 256 x 128 exponentials take 2,048
 // cycles a scheduler, the MMAs about 1,300; the row warps need 3,970 cycles a
-// tile.  512 tokens x 32 heads over 8,704 rows: 386 us on mma.sync, 94 here.
+// tile.  512 tokens x 32 heads over 8,704 rows: 386 us on mma.sync, 94 here;
+// 718 columns of D = 64 over 16,000 rows 79 against 21.
 // Every wait is bounded as in the attention on tcgen05.
 #pragma once
 #include "cache8_prefill_tc.cuh"
@@ -38,8 +39,9 @@ enum {
   kWbN = 14
 };
 
+template <int D>
 struct CwSmem {
-  static constexpr int kTile = 2 * 128 * 128;           // [panel][128 rows][128 B]
+  static constexpr int kTile = D / 64 * 128 * 128;      // [panel][128 rows][128 B]
   static constexpr int kQ = 2 * kTile;                  // behind K's two tiles: two slots
   static constexpr int kBars = kQ + 2 * kTile;
   static constexpr int kMisc = kBars + kWbN * 8;        // TMEM slot, fail
@@ -47,13 +49,14 @@ struct CwSmem {
   static constexpr int kConst = kMisc + 16;
   static constexpr int kBytes = 1024 + kConst + 4 * 4 * kCwCols * 4;
 };
-static_assert(CwSmem::kConst % 16 == 0, "vector loads");
+static_assert(CwSmem<64>::kConst % 16 == 0 && CwSmem<128>::kConst % 16 == 0, "vector loads");
 
 // Q as the weight kernel reads it: q16[b][g][column][D] fp16, factor[b][g][column] its power of two
 // times scale_log2.  grid ceil(B * T * H_q / 8), block 256, a warp a column.
+template <int D>
 __global__ void __launch_bounds__(256)
 cache8_q16_kernel(Attend8Args a, int batch, __half *__restrict__ q16, float *__restrict__ factor) {
-  constexpr int D = 128;
+  constexpr int E = D / 32;  // elements a lane
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x % 32, cols = a.T * a.G;
@@ -62,16 +65,20 @@ cache8_q16_kernel(Attend8Args a, int batch, __half *__restrict__ q16, float *__r
   const int col = static_cast<int>(i % cols), g = static_cast<int>(i / cols % a.H_kv);
   const int b = static_cast<int>(i / cols / a.H_kv), t = col_token(a, col);
   const int64_t row = (static_cast<int64_t>(b) * a.T + t) * a.H_kv * a.G + g * a.G + col - t * a.G;
-  const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.Q) + row * D + 4 * lane);
-  const float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
-  float mx = 0.0f;
+  const uint32_t *src = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.Q) + row * D + E * lane);
+  float x[E], mx = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) mx = fmaxf(mx, finite_abs(x[e]));
+  for (int e = 0; e < E; e += 2) {
+    const uint32_t w = src[e / 2];
+    x[e] = __uint_as_float(w << 16);
+    x[e + 1] = __uint_as_float(w & 0xffff0000u);
+    mx = fmaxf(mx, fmaxf(finite_abs(x[e]), finite_abs(x[e + 1])));
+  }
   mx = warp_max(mx);
   const float p2 = mx > 0.0f ? floor_pow2(mx) : 1.0f, inv = 1.0f / p2;
-  *reinterpret_cast<uint2 *>(q16 + i * D + 4 * lane) =
-      make_uint2(pack_f16x2(x[0] * inv, x[1] * inv), pack_f16x2(x[2] * inv, x[3] * inv));
+  uint32_t *dst = reinterpret_cast<uint32_t *>(q16 + i * D + E * lane);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_f16x2(x[e] * inv, x[e + 1] * inv);
   if (lane == 0) factor[i] = a.scale_log2 * p2;
 }
 
@@ -84,11 +91,10 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
-template <int FMT>
+template <int D, int FMT>
 __global__ void __launch_bounds__(kCwThreads, 1)
 cache8_weight_tc_kernel(Attend8Args a, const __half *__restrict__ q16, const float *__restrict__ factor) {
-  using Sm = CwSmem;
-  constexpr int D = 128;
+  using Sm = CwSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -151,10 +157,10 @@ cache8_weight_tc_kernel(Attend8Args a, const __half *__restrict__ q16, const flo
       const __half *src = q16 + (first + j * kCwCols) * D;
       const uint32_t dst = smem_u32(sm + Sm::kQ + (j & 1) * Sm::kTile);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {  // 16-byte pieces, sixteen a column
-        const int p = r + 128 * i, c = p >> 4;
+      for (int i = 0; i < D / 8; ++i) {  // 16-byte pieces, D / 8 a column
+        const int p = r + 128 * i, c = p / (D / 8);
         const bool have = j * kCwCols + c < cols;
-        cp_async_16(dst + ptc_swz(c, p & 15, kCwCols), src + (have ? p * 8 : 0), have);
+        cp_async_16(dst + ptc_swz(c, p % (D / 8), kCwCols), src + (have ? p * 8 : 0), have);
       }
       cp_async_commit();
       float *c = consts(j) + r;
@@ -203,10 +209,10 @@ cache8_weight_tc_kernel(Attend8Args a, const __half *__restrict__ q16, const flo
   } else {
     // ------------------------------------------------------------ rows
     const int x = warp >> 2, r = threadIdx.x & 127, row = r0 + 128 * x + r;
-    // K: 16-byte pieces of 256 rows, eight a thread, widened; rows past the last one are zero
+    // K: 16-byte pieces of 256 rows, D / 16 a thread, widened; rows past the last one are zero
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int p = static_cast<int>(threadIdx.x) + 256 * i, kr = p >> 3, pc = p & 7;
+    for (int i = 0; i < D / 16; ++i) {
+      const int p = static_cast<int>(threadIdx.x) + 256 * i, kr = p / (D / 16), pc = p % (D / 16);
       uint4 y = make_uint4(0, 0, 0, 0);
       if (r0 + kr < q.len) y = ld_stream16(a.k8 + (bh * a.cap + r0 + kr) * D + 16 * pc);
       uint32_t z[8];

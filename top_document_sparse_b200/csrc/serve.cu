@@ -249,7 +249,8 @@ struct Attend8Plan {
 
 // Columns from which the weights' second pass runs on tcgen05, which takes tiles of 128 of them.
 // tcgen05 against mma.sync: at 96 columns 14 against 21 us for one shape of 8,192 rows and 89 against
-// 97 us for 16 of 4,096; at 48 columns 14 against 16 us and 88 against 66 us.
+// 97 us for 16 of 4,096 (D = 64: 12 against 15 and 71 against 82); at 48 columns 14 against 16 us and
+// 88 against 66 us.
 constexpr int64_t kWeightTcCols = 96;
 
 // Partial results of the splits, and the softmaxes' statistics where weights are tracked.
@@ -267,7 +268,7 @@ void plan_attend8_scratch(Attend8Plan &p, const msa_memory *mem, const msa_cache
       p.scores = p.bytes;
       p.bytes += round256(static_cast<size_t>(c->batch) * mem->H_kv * c->capacity * p.score_w * 4);
     }
-    p.weight_tc = mem->dtype == MSA_BF16 && mem->D == 128 && static_cast<int64_t>(cols) >= kWeightTcCols;
+    p.weight_tc = mem->dtype == MSA_BF16 && static_cast<int64_t>(cols) >= kWeightTcCols;
     if (p.weight_tc) {
       p.q16 = p.bytes;
       p.factor = p.q16 + round256(rows * mem->D * 2);
@@ -403,17 +404,17 @@ msa_status launch_attend8(const msa::Attend8Args &a, const Attend8Plan &p, int B
                                : msa::cache8_weight_scores_kernel<16>;
     MSA_CUDA(launch_pdl(sk, dim3((a.cap + 255) / 256, B * a.H_kv), dim3(256), 0, st, a));
     MSA_LAUNCHED("cache8_weight_scores_kernel");
-  } else if (kBf16 && D == 128 && a.weights && p.weight_tc) {
-    auto wk = msa::cache8_weight_tc_kernel<FMT>;
+  } else if (kBf16 && a.weights && p.weight_tc) {
+    auto wk = msa::cache8_weight_tc_kernel<D, FMT>;
     auto *q16 = reinterpret_cast<__half *>(ws + p.q16);
     auto *factor = reinterpret_cast<float *>(ws + p.factor);
     const int64_t cols = static_cast<int64_t>(B) * a.T * a.H_kv * a.G;
-    MSA_CUDA(launch_pdl(msa::cache8_q16_kernel, dim3(static_cast<unsigned>((cols + 7) / 8)), dim3(256), 0,
+    MSA_CUDA(launch_pdl(msa::cache8_q16_kernel<D>, dim3(static_cast<unsigned>((cols + 7) / 8)), dim3(256), 0,
                         st, a, B, q16, factor));
     MSA_LAUNCHED("cache8_q16_kernel");
-    MSA_CUDA(allow_smem(wk, msa::CwSmem::kBytes));
+    MSA_CUDA(allow_smem(wk, msa::CwSmem<D>::kBytes));
     MSA_CUDA(launch_pdl(wk, dim3((a.cap + msa::kCwRows - 1) / msa::kCwRows, B * a.H_kv),
-                        dim3(msa::kCwThreads), msa::CwSmem::kBytes, st, a,
+                        dim3(msa::kCwThreads), msa::CwSmem<D>::kBytes, st, a,
                         static_cast<const __half *>(q16), static_cast<const float *>(factor)));
     MSA_LAUNCHED("cache8_weight_tc_kernel");
   } else if constexpr (NT == (kBf16 ? 4 : 2)) {  // (fewer columns left their scores behind)
