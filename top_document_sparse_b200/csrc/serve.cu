@@ -116,13 +116,15 @@ msa_status launch_rope(const msa_rope *rope, int64_t tokens, const int64_t *pos,
   const int half = rope->r / 2;
   const int rot = (V == 1 || !INTER) ? half / V : rope->r / V;
   const int rest = copy_rest ? (rope->D - rope->r) / V : 0;
-  // tokens a CTA: enough tasks for every thread
   // Small CTAs overlap one another's angles and copies best: 16,384 tokens of 40 heads of 128 take
   // 60 us at 64 threads, 64 at 128, 66 at 160, 68 to 84 at 256.  With few tokens a thread a task is
-  // faster (64 tokens: 2.1 us at 320 threads, 3.8 at 64).
+  // faster (64 tokens: 2.1 us at 320 threads, 3.8 at 64).  A CTA takes tokens for five tasks a thread
+  // (75,000 tokens of 3 heads of 64, half of each rotated: 20 us, with one task 27; 30,000 fp32 tokens
+  // of 10 heads of 64: 30, with four 35), but 16 at most, whose angles take longer than a lone head's
+  // copies (100,000 tokens of one head of 64: 15 us, with 40 tokens 21).
   const int per_token = (q.heads + k.heads) * (rot + rest);
   const bool few = tokens * round32(per_token) < 2048LL * num_sms();
-  const int tok = std::max(1, std::min(16, (few ? 256 : 64) / std::max(per_token, 1)));
+  const int tok = std::max(1, std::min(16, (few ? 256 : 320) / per_token));
   const int threads = few ? std::min(round32(tok * per_token), msa::kRopeThreads) : 64;
   const int64_t grid = (tokens + tok - 1) / tok;
   if (grid > 0x7FFFFFFF) return fail(MSA_ERR_UNSUPPORTED, "too many tokens");
