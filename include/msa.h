@@ -699,7 +699,7 @@ MSA_API msa_status msa_cache8_evict(const msa_memory *mem, const msa_cache8 *cac
                                     const msa_cache8 *out, int32_t budget, int32_t recent,
                                     void *workspace, size_t workspace_bytes, msa_stream stream);
 
-/* Read and clear the device error word of the current device (synchronises/* Read and clear the device error word of the current device (synchronises/* Read and clear the device error word of the current device (synchronises
+/* Read and clear the device error word of the current device (synchronises
  * `stream`).  *bits receives the MSA_DEVERR_* bits; returns MSA_ERR_TIMEOUT or
  * MSA_ERR_STATE when a bit was set, else MSA_OK. */
 MSA_API msa_status msa_device_error(uint32_t *bits, msa_stream stream);

@@ -249,7 +249,8 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
           const int col = c0 + (warp >> 2) * kC8tRows + r0 + 2 * (i0 + i);
           w[i] = make_uint4(0, 0, 0, 0);
           if (col < cols)
-            w[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.Q) + static_cast<int64_t>(row_of(col)) * D) + piece);
+            w[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.Q) +
+                                                         static_cast<int64_t>(row_of(col)) * D) + piece);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
