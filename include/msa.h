@@ -691,7 +691,8 @@ MSA_API size_t msa_cache8_evict_workspace_size(const msa_memory *mem, const msa_
  *         buffers do not overlap and whose capacity is >= min(capacity,
  *         budget); it needs weights too.  Its weights of rows that the query
  *         no longer holds become 0; its other bytes there stay.
- *   budget >= block_len; 0 <= recent <= budget
+ *   budget >= block_len; 0 <= recent <= budget (beyond the capacity they mean
+ *   the capacity: 2^31 - 1 for both keeps every row)
  * A length outside [0, capacity] is flagged (MSA_DEVERR_BAD_LENGTH) and taken
  * as the nearer bound.
  */

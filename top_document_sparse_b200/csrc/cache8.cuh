@@ -356,7 +356,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// What an eviction keeps of one query: full blocks, recent ones among them, new length.
+// What an eviction keeps of one query: full blocks, recent ones among them, new length.  The host
+// keeps budget and recent within the capacity; 0 <= recent <= keep <= full, so the list of kept
+// blocks fits its nb + 1 entries.
 struct EvictPlan {
   int len, full, tail, keep, recent, new_len;
 };
@@ -366,7 +368,7 @@ __device__ __forceinline__ EvictPlan evict_plan(int len, int cap, int bl, int bu
   p.full = p.len / bl;
   p.tail = p.len % bl;
   p.keep = p.len > budget ? (budget - p.tail) / bl : p.full;
-  p.recent = min((recent + bl - 1) / bl, p.keep);
+  p.recent = min(recent / bl + (recent % bl != 0 ? 1 : 0), p.keep);
   p.new_len = p.keep * bl + p.tail;
   return p;
 }

@@ -703,6 +703,9 @@ msa_status msa_cache8_evict(const msa_memory *mem, const msa_cache8 *cache, cons
       in_place != (out->v_scale == cache->v_scale) || in_place != (out->weights == cache->weights) ||
       in_place != (out->cache_len == cache->cache_len) || (in_place && out->capacity != cache->capacity))
     return fail(MSA_ERR_INVALID_ARG, "out must be the same cache or share no buffer with it");
+  // beyond the capacity they mean the capacity (2^31 - 1: keep everything)
+  budget = std::min(budget, cache->capacity);
+  recent = std::min(recent, budget);
   const EvictPlan8 p = plan_evict8(mem, cache);
   if (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)
     return fail(MSA_ERR_INVALID_ARG, "workspace missing, unaligned or too small: %zu < %zu",
@@ -740,7 +743,7 @@ msa_status msa_cache8_evict(const msa_memory *mem, const msa_cache8 *cache, cons
   m.bl = bl;
   m.D = mem->D;
   const int streams = 2 * (bl * mem->D / 16) + bl / 4 + 2;
-  const int live = (std::min(budget, cache->capacity) + bl - 1) / bl;
+  const int live = (budget + bl - 1) / bl;
   const int parts = in_place ? 1 : std::max(1, std::min(live / msa::kMoveWave, 65535));
   MSA_CUDA(launch_pdl(msa::cache8_move_kernel, dim3((streams + 127) / 128, bh, parts), dim3(128), 0,
                       st, m, static_cast<const int32_t *>(src), static_cast<const int32_t *>(lens),
