@@ -43,6 +43,7 @@ namespace msa {
 constexpr int kC8Warps = 4;
 constexpr int kC8Stages = 3;          // tiles of a warp in flight or in use
 constexpr float kC8Shift = 11.0f;     // P is 2^11 exp2(s - m)
+constexpr float kC8Top = 2048.0f;     // 2^kC8Shift
 constexpr float kC8Slack = 4.0f;      // a score may exceed m by this before m moves,
 constexpr float kC8Lead = 8.0f;       // and m then moves this far above it
 constexpr float kC8MinUnit = 0x1p-60f;  // smallest unit of O
@@ -332,14 +333,17 @@ struct Softmax8 {
           for (int e = 0; e < 4; ++e) acc[nt][i][e] *= f;
     }
   }
-  // s (log2 units, -inf where hidden) -> p = 2^(s - m + shift), the sums and, where a score
-  // passes its column's reference by more than the slack, new references
+  // s (log2 units, -inf where hidden) -> p = 2^(s - m), the sums and, where a score passes its
+  // column's reference by more than the slack, new references.  The difference comes first and is
+  // compared itself: of scores so large that a unit is below their rounding, s - (m - c) and s > m + c
+  // would be off by that rounding, and p could leave fp16.  (For the same reason a score's product is
+  // rounded by itself, never fused with what is subtracted.)
   __device__ __forceinline__ void step(float (&s)[NT][4]) {
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) over = over || s[nt][e] > m[nt][e & 1] + kC8Slack;
+      for (int e = 0; e < 4; ++e) over = over || s[nt][e] - m[nt][e & 1] > kC8Slack;  // (-inf - -inf: false)
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -349,7 +353,7 @@ struct Softmax8 {
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          const float mn = v > m[nt][h] + kC8Slack ? v + kC8Lead : m[nt][h];
+          const float mn = v - m[nt][h] > kC8Slack ? v + kC8Lead : m[nt][h];
           const float f = mn == m[nt][h] ? 1.0f : ex2_approx(m[nt][h] - mn);
           m[nt][h] = mn;
           l[nt][h] *= f;
@@ -365,7 +369,7 @@ struct Softmax8 {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // a column that has seen nothing: -inf - 0, weight 0
-        const float base = (m[nt][h] == -INFINITY ? 0.0f : m[nt][h]) - kC8Shift;
+        const float base = m[nt][h] == -INFINITY ? 0.0f : m[nt][h];
         s[nt][h] = ex2_approx(s[nt][h] - base);
         s[nt][2 + h] = ex2_approx(s[nt][2 + h] - base);
         l[nt][h] += s[nt][h] + s[nt][2 + h];
@@ -549,7 +553,7 @@ cache8_attend_kernel(Attend8Args a) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] *= colf[nt][e & 1] * k_scale;
+      for (int e = 0; e < 4; ++e) s[nt][e] = __fmul_rn(s[nt][e], colf[nt][e & 1] * k_scale);
     if (x0 + 16 > all_see) {  // rows that some column does not see
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -568,7 +572,7 @@ cache8_attend_kernel(Attend8Args a) {
     }
     st.step(s);
     st.raise_unit(v_scale);
-    const float ratio = v_scale * st.inv_unit;
+    const float ratio = v_scale * st.inv_unit * kC8Top;
     uint32_t pb[NT][2], pt[F32 ? NT : 1][2];  // P, and of fp32 its tail
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -616,7 +620,7 @@ cache8_attend_kernel(Attend8Args a) {
   const int m1 = share(nm, ms + 1, mn);
   const __nv_bfloat16 *qb = reinterpret_cast<const __nv_bfloat16 *>(sm + Sm::kQb);
   const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
-  const float to_unit = st.inv_unit;
+  const float to_unit = st.inv_unit * kC8Top;
   for (int mt = share(nm, ms, mn) + warp; mt < m1; mt += kC8Warps) {
     const int x0 = mt * 16;
     auto row_ptr = [&](int x) {
@@ -649,7 +653,7 @@ cache8_attend_kernel(Attend8Args a) {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[nt][e] = x0 + lg + 8 * (e >> 1) < n_mem ? s[nt][e] * a.scale_log2 : -INFINITY;
+        s[nt][e] = x0 + lg + 8 * (e >> 1) < n_mem ? __fmul_rn(s[nt][e], a.scale_log2) : -INFINITY;
       }
     st.step(s);
     uint32_t pb[NT][2][2];  // [part][row half]
@@ -689,7 +693,7 @@ cache8_attend_kernel(Attend8Args a) {
   cp_async_wait<0>();
   __syncthreads();  // every warp is done with its ring
   float *merge = reinterpret_cast<float *>(sm + Sm::kMerge);
-  const float out = st.unit * exp2f(-kC8Shift);
+  const float out = st.unit / kC8Top;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -706,7 +710,7 @@ cache8_attend_kernel(Attend8Args a) {
       }
       if (lg == 0) {
         row[D] = st.m[nt][h];
-        row[D + 1] = L * exp2f(-kC8Shift);
+        row[D + 1] = L;
       }
     }
   __syncthreads();
@@ -1035,7 +1039,8 @@ struct WeightColumns {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float p = ex2_approx(s[nt][e] * (cf[nt][e & 1] * k_scale) - ml[nt][e & 1].x);
+        // (the attention's product, rounded before the reference leaves it, as there)
+        float p = ex2_approx(__fmul_rn(s[nt][e], cf[nt][e & 1] * k_scale) - ml[nt][e & 1].x);
         if (masked && x0 + lg + 8 * (e >> 1) >= rows[nt][e & 1]) p = 0.0f;
         sum[e >> 1] = fmaf(p, ml[nt][e & 1].y, sum[e >> 1]);
       }

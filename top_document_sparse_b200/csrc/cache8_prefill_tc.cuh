@@ -44,6 +44,7 @@ constexpr int kC8tThreads = 32 * 10 + kC8tConv;
 constexpr int kC8tBlk = 64;                         // context rows per block
 constexpr int kC8tSlots = 4;                        // ring of K, ring of V
 constexpr int kC8tRows = 128;                       // columns per tile (UMMA M)
+constexpr float kC8tFar = 2048.0f;                  // scores (log2 units) beyond this are "far"
 constexpr uint32_t kC8tTmemCols = 512;              // S, then P, of tile x at 128 x + 64 (block % 2),
 constexpr uint32_t kC8tTmemO = 256;                 // O of tile x at 256 + 128 x
 
@@ -528,19 +529,21 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       for (int i = 0; i < kC8tBlk; i += 8)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
-      const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
-      const float m_new = bm > m_run + kC8Slack ? bm + kC8Lead : m_run;
+      const float bm = __fmul_rn(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c);
+      const float m_new = bm - m_run > kC8Slack ? bm + kC8Lead : m_run;  // (-inf - -inf: no)
       float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
-      const float mo = (m_new == -INFINITY ? 0.0f : m_new) - kC8Shift;
+      float ref = m_new == -INFINITY ? 0.0f : m_new;
+      if (fabsf(ref) > kC8tFar) {
+        // far scores: the reference came from a rounded product, so the others are rounded alike, and
+        // it leaves them before small terms are added that their rounding would swallow
+#pragma unroll
+        for (int i = 0; i < kC8tBlk; ++i) s[i] = __fmul_rn(s[i], c) - ref;
+        c = 1.0f;
+        ref = 0.0f;
+      }
       // the ratio of the scales in the exponent, unless it would take weights out of range
       const bool fold = lr >= -24;
-      const float mf = fold ? mo - static_cast<float>(lr) : mo;
-      if (fabsf(m_new) > 262144.0f && m_new != -INFINITY) {
-        // far scores: the reference came from a rounded product, so the others are rounded alike
-#pragma unroll
-        for (int i = 0; i < kC8tBlk; ++i) s[i] = __fmul_rn(s[i], c);
-        c = 1.0f;
-      }
+      const float mf = ref - kC8Shift - (fold ? static_cast<float>(lr) : 0.0f);
       l_run *= alpha;
       alpha *= unit / unit_new;
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {

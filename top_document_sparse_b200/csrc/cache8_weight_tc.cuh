@@ -47,7 +47,8 @@ struct CwSmem {
   static constexpr int kMisc = kBars + kWbN * 8;        // TMEM slot, fail
   // per column, a ring of four tiles: factor, -reference, 1 / L, visible rows
   static constexpr int kConst = kMisc + 16;
-  static constexpr int kBytes = 1024 + kConst + 4 * 4 * kCwCols * 4;
+  static constexpr int kFar = kConst + 4 * 4 * kCwCols * 4;  // a ring of four: [copier warp] far scores
+  static constexpr int kBytes = 1024 + kFar + 4 * 16;
 };
 static_assert(CwSmem<64>::kConst % 16 == 0 && CwSmem<128>::kConst % 16 == 0, "vector loads");
 
@@ -168,6 +169,8 @@ cache8_weight_tc_kernel(Attend8Args a, const __half *__restrict__ q16, const flo
       c[kCwCols] = -ml.x;
       c[2 * kCwCols] = ml.y;
       c[3 * kCwCols] = __int_as_float(real ? column_rows(a, q, col) : 0);
+      const bool far = __any_sync(0xffffffffu, fabsf(ml.x) > kC8tFar && ml.x != INFINITY);
+      if (lane == 0) reinterpret_cast<int *>(sm + Sm::kFar)[4 * (j & 3) + warp - 9] = far;
       cp_async_wait<0>();
       fence_proxy_async_smem();  // the tile becomes visible to the tensor cores
       mbar_arrive(bar(kWbFullQ0 + (j & 1)));
@@ -237,6 +240,8 @@ cache8_weight_tc_kernel(Attend8Args a, const __half *__restrict__ q16, const flo
       const float *c = consts(j);
       // hidden rows only where the tile passes what the first column sees
       const bool masked = last >= column_rows(a, q, j * kCwCols);
+      const int4 fr = *reinterpret_cast<const int4 *>(sm + Sm::kFar + 16 * (j & 3));
+      const bool far = (fr.x | fr.y | fr.z | fr.w) != 0;
 #pragma unroll
       for (int h = 0; h < kCwCols; h += 32) {
         uint32_t raw[32];
@@ -252,8 +257,17 @@ cache8_weight_tc_kernel(Attend8Args a, const __half *__restrict__ q16, const flo
                            make_float2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])));
           float2 e1 = mul2(mul2(make_float2(cf.z, cf.w), k2),
                            make_float2(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3])));
-          e0 = add2(e0, make_float2(nm.x, nm.y));
-          e1 = add2(e1, make_float2(nm.z, nm.w));
+          if (far) {
+            // the product rounded by itself, as in the attention (above it is fused with the sum):
+            // a far score's rounding is many times a unit of its exponent
+            e0.x = __fadd_rn(__fmul_rn(__fmul_rn(cf.x, ks), __uint_as_float(raw[i])), nm.x);
+            e0.y = __fadd_rn(__fmul_rn(__fmul_rn(cf.y, ks), __uint_as_float(raw[i + 1])), nm.y);
+            e1.x = __fadd_rn(__fmul_rn(__fmul_rn(cf.z, ks), __uint_as_float(raw[i + 2])), nm.z);
+            e1.y = __fadd_rn(__fmul_rn(__fmul_rn(cf.w, ks), __uint_as_float(raw[i + 3])), nm.w);
+          } else {
+            e0 = add2(e0, make_float2(nm.x, nm.y));
+            e1 = add2(e1, make_float2(nm.z, nm.w));
+          }
           float2 p0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
           float2 p1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
           if (masked) {
