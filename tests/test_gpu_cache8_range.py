@@ -34,14 +34,157 @@ def test_evict_with_budgets_beyond_the_capacity(budget, recent, in_place):
     assert msa.device_error() == 0
 
 
-# ---------------------------------------------------------------- attention
+# ---------------------------------------------------------------- attention, bounds by row
+U = 2.0 ** -23
+QMAX = {"int8": 127.0, "e4m3": 448.0}
+
+
+def expected(ref, mem_rows, Q, n, bf16):
+    """O, lse, weights and their bounds in fp64.  First order in u = 2^-23, for each column by itself:
+      ds_j = (D + 17) u sum_d |q_d k_jd| / sqrt(D)  (sums on the tensor cores may truncate)
+             + sum_d (lost(q_d) |k_jd| + [memory row] lost(k_jd) |q_d|) / sqrt(D)
+      lost : 2^-25 of a row's largest element for elements whose bits reach below fp16's smallest
+             step there: bf16's 8 bits below 2^-16 of the largest, fp32's all (zeros lose nothing)
+      dl   = sum_j p_j ds_j + (rows + 8) u                        of the log-sum
+      O    : sum_j p_j |v_j| (ds_j + dl + w + (rows + 16) u), w the rounding of a weight: 2^-11 to
+             fp16 (bf16 queries), 2^-22 to its head and tail (fp32)
+             + 2^-28 P sum_j |v_j| / s_j: weights below fp16's normal range, half its smallest step
+             2^-25 against weights times scales kept at 2^11 2^-8 of P = max_j p_j s_j or above
+             + 2^-25 sum_(memory rows) p_j max|v_j|                a bf16 row as fp16
+    A scale s_j of a memory row is the power of two at or below its largest element.  A block or a
+    row of little weight enters by that weight alone, however large its values are."""
+    B, T, Hq, D = Q.shape
+
+    def lost(x):
+        a = np.abs(x)
+        top = a.max(-1, initial=0.0, keepdims=True)
+        return np.where((a > 0) & ((a < 2.0 ** -16 * top) | (not bf16)), 2.0 ** -25 * top, 0.0)
+
+    G, w = Hq // ref.H, 2.0 ** -11 if bf16 else 2.0 ** -22
+    O, tol = np.zeros(Q.shape), np.zeros(Q.shape)
+    lse, tl = np.zeros((B, T, Hq)), np.zeros((B, T, Hq))
+    W, tw = np.zeros((B, ref.H, ref.cap)), np.zeros((B, ref.H, ref.cap))
+    for b in range(B):
+        ln = int(ref.lens[b])
+        for g in range(ref.H):
+            M = mem_rows[b][0].shape[0]
+            K = np.concatenate([mem_rows[b][0][:, g], ref.values(b, g, "k")])
+            V = np.concatenate([mem_rows[b][1][:, g], ref.values(b, g, "v")])
+            top = np.abs(V[:M]).max(1, initial=0.0)
+            s = np.concatenate([2.0 ** np.floor(np.log2(np.maximum(top, 1e-30))),
+                                np.repeat(ref.vs[b, g], ref.bl)[:ln]])
+            vq = np.where(s[:, None] > 0, np.abs(V) / np.where(s > 0, s, 1.0)[:, None], 0.0)
+            kl = np.concatenate([lost(K[:M]), np.zeros((ln, D))])
+            for t in range(int(n[b])):
+                seen = M + max(0, ln - int(n[b]) + t + 1)
+                rows = seen
+                for h in range(g * G, (g + 1) * G):
+                    q = Q[b, t, h]
+                    if seen == 0:
+                        lse[b, t, h] = -np.inf
+                        continue
+                    z = K[:seen] @ q / D ** 0.5
+                    ds = ((D + 17) * U * (np.abs(K[:seen]) @ np.abs(q)) + np.abs(K[:seen]) @ lost(q)
+                          + kl[:seen] @ np.abs(q)) / D ** 0.5
+                    p = np.exp(z - z.max())
+                    lse[b, t, h] = z.max() + np.log(p.sum())
+                    p /= p.sum()
+                    dl = p @ ds + (rows + 8) * U
+                    a = np.abs(V[:seen])
+                    O[b, t, h] = p @ V[:seen]
+                    tol[b, t, h] = ((p * (ds + dl + w + (rows + 16) * U)) @ a
+                                    + 2.0 ** -28 * (p * s[:seen]).max() * vq[:seen].sum(0)
+                                    + 2.0 ** -25 * (p[:M] @ top))
+                    tl[b, t, h] = dl + 4 * U * abs(lse[b, t, h])
+                    W[b, g, :seen - M] += p[M:]
+                    tw[b, g, :seen - M] += p[M:] * (ds[M:] + tl[b, t, h] + 16 * U)
+    if bf16:
+        tol = tol + 2.0 ** -8 * (np.abs(O) + tol)
+    return O, tol, lse, tl, W, tw
+
+
+def check_attend(mem, content, cache, Q, ids=None):
+    from top_document_sparse_b200 import msa
+    import cache8_ref as R
+    B, T, Hq, D = Q.shape
+    ref = R.RefCache(B, mem.n_kv_heads, cache.capacity, D, cache.block_len, cache.fmt).load(cache)
+    rows = R.content_rows(mem, content, ids) if ids is not None else \
+        [(np.zeros((0, mem.n_kv_heads, D)),) * 2] * B
+    k = 0 if ids is None else ids.shape[1]
+    O, lse = torch.empty_like(Q), torch.empty(B, T, Hq, device="cuda")
+    cache.attend(content, ids, Q, O, msa.workspace(cache.attend_workspace_size(T, k, Hq)), lse=lse,
+                 weight_decay=None if cache.weights is None else 0.0)
+    want, tol, wl, tl, W, tw = expected(ref, rows, f64(Q), [T] * B, Q.dtype == torch.bfloat16)
+    err = np.abs(f64(O) - want)
+    assert np.all(err <= tol), f"O off by {np.nanmax(err / np.maximum(tol, 1e-300)):.3g} times its bound"
+    assert np.all(np.abs(f64(lse) - wl) <= tl)
+    if cache.weights is not None:
+        for b in range(B):
+            n = int(ref.lens[b])
+            assert np.all(np.abs(f64(cache.weights[b, :, :n]) - W[b, :, :n]) <= tw[b, :, :n] + 2.0 ** -100)
+    assert msa.device_error() == 0
+
+
 # dtype, D, tokens, heads of a group: one MMA column tile, two, four, tcgen05, fp32 of one and two
 PATHS = [("bf16", 128, 1, 4), ("bf16", 64, 3, 4), ("bf16", 64, 20, 2), ("bf16", 128, 30, 2), ("bf16", 128, 150, 1),
          ("f32", 64, 1, 2), ("f32", 128, 6, 2)]
 
 
+MMA_SYNC = [p for p in PATHS if p[1] * p[2] < 2000]
+
+
 def torch_dtype(dt):
     return torch.bfloat16 if dt == "bf16" else torch.float32
+
+
+def rows_and_queries(dt, D, T, G, n, seed):
+    """K, V of n rows and T x G queries; dimension 0 of every query is 8, dimension 1 is 0."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    kv = torch.randn(2, 1, n, 1, D, generator=g, device="cuda")
+    Q = torch.randn(1, T, G, D, generator=g, device="cuda")
+    kv[0, ..., :2] = 0.0
+    Q[..., 0], Q[..., 1] = 8.0, 0.0
+    return kv, Q
+
+
+def light(K, rows, D, log2_weight=60.0):
+    """K[rows] such that every query gives them 2^-log2_weight of an ordinary row's weight."""
+    K[:, rows, :, 0] = -log2_weight * 0.6931 * D ** 0.5 / 8.0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("path", MMA_SYNC, ids=lambda p: "-".join(map(str, p)))
+@pytest.mark.parametrize("r", [0, 16, 24, 28, 60])
+def test_attend_after_a_light_block_of_huge_values(path, fmt, r):
+    """Blocks whose V is 2^r times the others' and whose weight is nothing, each followed by an
+    ordinary one, so that every warp of every split meets both, the light one first."""
+    from top_document_sparse_b200 import msa
+    dt, D, T, G = path
+    mem, content = memory(torch_dtype(dt), 1, D)
+    n = 8192
+    kv, Q = rows_and_queries(dt, D, T, G, n, seed=r + D)
+    for x in range(0, n, 128):
+        light(kv[0], slice(x, x + 64), D)
+        kv[1, :, x:x + 64] *= 2.0 ** r
+    cache = msa.Cache8(mem, 1, n, 64, fmt)
+    cache.append(kv[0].to(mem.dtype), kv[1].to(mem.dtype))
+    check_attend(mem, content, cache, Q.to(mem.dtype))
+
+
+@pytest.mark.parametrize("path", MMA_SYNC, ids=lambda p: "-".join(map(str, p)))
+@pytest.mark.parametrize("small", [2.0 ** -27, 2.0 ** -100])
+def test_attend_after_a_block_of_zeros(path, small):
+    """All-zero rows (they carry weight) before and among rows of small V."""
+    from top_document_sparse_b200 import msa
+    dt, D, T, G = path
+    mem, content = memory(torch_dtype(dt), 1, D)
+    kv, Q = rows_and_queries(dt, D, T, G, 192 + T, seed=D)
+    kv[1] *= small
+    kv[:, :, :64] = 0.0
+    kv[:, :, 80:96] = 0.0
+    cache = msa.Cache8(mem, 1, 512, 16, "int8")
+    cache.append(kv[0].to(mem.dtype), kv[1].to(mem.dtype))
+    check_attend(mem, content, cache, Q.to(mem.dtype))
 
 
 @pytest.mark.parametrize("path", PATHS, ids=lambda p: "-".join(map(str, p)))

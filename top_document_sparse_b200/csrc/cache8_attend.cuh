@@ -17,19 +17,24 @@
 // interleaved by byte permutes).
 //   Widening: int8 and e4m3 values are exact in fp16, so both MMAs are fp16
 // with the block's scale applied outside: K's to the score; V's to P, as its
-// ratio to the largest V scale seen so far (r), O being kept in units of r.
+// ratio 2^r to the largest V scale seen so far (the unit), r <= 0.
 // int8 -> fp16 is a byte permute that sets the bits of 1024 + (q + 128) and
-// one subtraction.  Q is scaled by a power of two per column to 1 <= max|q| < 2, which loses
-// nothing of a bf16 row down to 2^-17 of its largest element.  P is kept at
-// 2^11 times its size against a reference that moves, to 8 above the score (log2
-// units), only when a score exceeds it by 4: at most 2^15, and weights down to
-// 2^-17 of the largest keep fp16's full 11 bits, smaller ones an error below
-// 2^-28 of the largest.
+// one subtraction.  Q is scaled by a power of two per column to 1 <= max|q| < 2: elements
+// below 2^-17 of the largest lose bits, 2^-25 of it at most.
+//   P = 2^(s - m + r + 11) in fp16 against a column's reference m, which moves, to
+// 7 to 8 above s + r (log2 units), only when that exceeds it by 4: P is at most 2^15,
+// weights whose product with the scale is down to 2^-17 of the column's largest keep fp16's
+// full 11 bits, smaller ones an error below 2^-28 of that product.  So m follows
+// what a block adds to O, not its scores alone, and when the unit grows m
+// falls by as much, so that O's own unit (m and the unit together) stays: a light block of huge values
+// costs the others nothing.  (With m following the scores, weights behind a block
+// of no weight and 2^24 times larger values kept 3 bits.)  The sum of the weights 2^(s - m) is fp32
+// and takes m's distance from the scores as it is, up to 2^100.
 //   Memory rows are bf16 and go through bf16 MMAs; P is split there into a bf16
 // head and tail, two MMAs, so it loses nothing either.
 //   fp32 queries run the same kernel with Q and P split into an fp16 head and
-// tail, two MMAs each: 2^-22 of the column's largest element is lost, as fp32
-// sums lose anyway.  fp32 memory rows have a kernel of their own on CUDA cores.
+// tail, two MMAs each: 2^-22 of a weight and 2^-25 of the column's largest element are lost.  fp32
+// memory rows have a kernel of their own on CUDA cores.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -44,9 +49,11 @@ constexpr int kC8Warps = 4;
 constexpr int kC8Stages = 3;          // tiles of a warp in flight or in use
 constexpr float kC8Shift = 11.0f;     // P is 2^11 exp2(s - m)
 constexpr float kC8Top = 2048.0f;     // 2^kC8Shift
-constexpr float kC8Slack = 4.0f;      // a score may exceed m by this before m moves,
-constexpr float kC8Lead = 8.0f;       // and m then moves this far above it
-constexpr float kC8MinUnit = 0x1p-60f;  // smallest unit of O
+constexpr float kC8Slack = 4.0f;      // s + r may exceed m by this before m moves,
+constexpr float kC8Lead = 7.0f;       // and m then moves this far above the next whole number
+constexpr float kC8MinRatio = -96.0f; // r as the references see it: a weight is 2^100 at most
+constexpr float kC8MaxSum = 110.0f;   // log2 to which a growing unit may raise a sum of weights
+constexpr float kC8None = -3e38f;     // the reference of a column that has seen nothing
 
 struct Attend8Args {
   const void *content;
@@ -298,20 +305,43 @@ __device__ __forceinline__ void load_q_columns(const Attend8Args &a, int b, int 
   }
 }
 
+// 2^x of a whole number x in [-127, 127], 0 for -127: x + 127 in the low bits of the sum.
+__device__ __forceinline__ float pow2_whole(float x) {
+  return __int_as_float(__float_as_int(x + (12582912.0f + 127.0f)) << 23);
+}
+// Exponent of a non-negative number (0: -127).
+__device__ __forceinline__ float exponent_of(float x) {
+  return static_cast<float>((__float_as_int(x) >> 23) - 127);
+}
+// r of a block of this V scale: log2 of the scale over the unit, as the references see it.
+__device__ __forceinline__ float scale_ratio(float scale, float unit) {
+  return scale > 0.0f ? fmaxf(exponent_of(scale) - exponent_of(unit), kC8MinRatio) : kC8MinRatio;
+}
+// A reference 7 to 8 above the largest s + r.  Scores so large that their rounding swallows r: no lower
+// than that (P stays in fp16, and loses bits where r is not 0).
+__device__ __forceinline__ float new_reference(float top, float r) {
+  return r == 0.0f ? ceilf(top) + kC8Lead : __fadd_ru(ceilf(top), r + kC8Lead);
+}
+// The unit grows by 2^up: how far the reference of a column with the sum l falls with it; the rest is
+// O's to lose.  (m is a whole number; where it is too large to fall, and before anything was seen, 0.)
+__device__ __forceinline__ float reference_falls(float m, float l, float up) {
+  const float k = fmaxf(fminf(fminf(up, kC8MaxSum - exponent_of(l)), 127.0f), 0.0f);
+  return m - (m - k) == k ? k : 0.0f;
+}
+
 // The running softmax of 8 NT columns over tiles of 16 context rows: lane (g, t) holds rows
 // g, g + 8 and columns 8 nt + 2t, + 1 of S^T.
 template <int D, int NT>
 struct Softmax8 {
   float m[NT][2], l[NT][2];
   float acc[NT][D / 16][4];  // O^T, [d pair][col pair], in units of `unit`
-  float unit, inv_unit;  // a power of two and its reciprocal, the same in every lane
+  float unit, inv_unit;  // a power of two and its reciprocal, the same in every lane (0: no V but zeros yet)
 
   __device__ __forceinline__ void init() {
-    unit = kC8MinUnit;
-    inv_unit = 1.0f / kC8MinUnit;
+    unit = inv_unit = 0.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kC8None;
       l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -319,31 +349,43 @@ struct Softmax8 {
         for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.0f;
     }
   }
-  // O's unit becomes at least v
+  // The unit becomes at least v: references fall and sums grow, O stays as it is (see above).
   __device__ __forceinline__ void raise_unit(float v) {
-    if (v > unit) {
-      const float f = unit / v;
-      unit = v;
-      inv_unit = 1.0f / v;
+    if (v <= unit) return;
+    const float up = exponent_of(v) - exponent_of(unit);
+    const bool first = unit == 0.0f;  // (O is 0, in any unit)
+    unit = v;
+    inv_unit = 1.0f / v;
+    if (!first) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+        for (int h = 0; h < 2; ++h) {
+          const float k = reference_falls(m[nt][h], l[nt][h], up), f = pow2_whole(fmaxf(k - up, -127.0f));
+          m[nt][h] -= k;
+          l[nt][h] *= pow2_whole(k);
+          if (k != up) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][i][e] *= f;
+            for (int i = 0; i < D / 16; ++i) {
+              acc[nt][i][h] *= f;
+              acc[nt][i][2 + h] *= f;
+            }
+          }
+        }
     }
   }
-  // s (log2 units, -inf where hidden) -> p = 2^(s - m), the sums and, where a score passes its
-  // column's reference by more than the slack, new references.  The difference comes first and is
+  // s (log2 units, -inf where hidden) of rows whose V scale is 2^r units -> p = 2^(s - m), the sums
+  // and, where s + r passes its column's reference by more than the slack, new references.  The difference comes first and is
   // compared itself: of scores so large that a unit is below their rounding, s - (m - c) and s > m + c
   // would be off by that rounding, and p could leave fp16.  (For the same reason a score's product is
   // rounded by itself, never fused with what is subtracted.)
-  __device__ __forceinline__ void step(float (&s)[NT][4]) {
+  __device__ __forceinline__ void step(float (&s)[NT][4], float r) {
+    const float lim = kC8Slack - r;
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) over = over || s[nt][e] - m[nt][e & 1] > kC8Slack;  // (-inf - -inf: false)
+      for (int e = 0; e < 4; ++e) over = over || s[nt][e] - m[nt][e & 1] > lim;
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -353,7 +395,7 @@ struct Softmax8 {
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          const float mn = v - m[nt][h] > kC8Slack ? v + kC8Lead : m[nt][h];
+          const float mn = v - m[nt][h] > lim ? new_reference(v, r) : m[nt][h];
           const float f = mn == m[nt][h] ? 1.0f : ex2_approx(m[nt][h] - mn);
           m[nt][h] = mn;
           l[nt][h] *= f;
@@ -368,10 +410,8 @@ struct Softmax8 {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        // a column that has seen nothing: -inf - 0, weight 0
-        const float base = m[nt][h] == -INFINITY ? 0.0f : m[nt][h];
-        s[nt][h] = ex2_approx(s[nt][h] - base);
-        s[nt][2 + h] = ex2_approx(s[nt][2 + h] - base);
+        s[nt][h] = ex2_approx(s[nt][h] - m[nt][h]);
+        s[nt][2 + h] = ex2_approx(s[nt][2 + h] - m[nt][h]);
         l[nt][h] += s[nt][h] + s[nt][2 + h];
       }
   }
@@ -511,6 +551,7 @@ cache8_attend_kernel(Attend8Args a) {
 
   // ---- local rows
   int stage = 0;
+  float scale = -1.0f, r = 0.0f, ratio = 0.0f;  // V's scale, log2 of it over the unit, P's factor
   for (; tile < l1; tile += kC8Warps) {
     const int next = tile + kC8Warps;
     cp_async_wait<kC8Stages - 2>();
@@ -570,9 +611,13 @@ cache8_attend_kernel(Attend8Args a) {
           *reinterpret_cast<float2 *>(out + 8 * a.score_w + 8 * nt) = make_float2(s[nt][2], s[nt][3]);
         }
     }
-    st.step(s);
-    st.raise_unit(v_scale);
-    const float ratio = v_scale * st.inv_unit * kC8Top;
+    if (v_scale != scale) {  // (neighbouring tiles mostly share one)
+      scale = v_scale;
+      st.raise_unit(scale);
+      r = scale_ratio(scale, st.unit);
+      ratio = scale * st.inv_unit * kC8Top;
+    }
+    st.step(s, r);
     uint32_t pb[NT][2], pt[F32 ? NT : 1][2];  // P, and of fp32 its tail
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -620,7 +665,9 @@ cache8_attend_kernel(Attend8Args a) {
   const int m1 = share(nm, ms + 1, mn);
   const __nv_bfloat16 *qb = reinterpret_cast<const __nv_bfloat16 *>(sm + Sm::kQb);
   const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
-  const float to_unit = st.inv_unit * kC8Top;
+  const bool any_mem = share(nm, ms, mn) + warp < m1;
+  if (any_mem) st.raise_unit(1.0f);  // (V as it is)
+  const float to_unit = st.inv_unit * kC8Top, mem_ratio = scale_ratio(1.0f, st.unit);
   for (int mt = share(nm, ms, mn) + warp; mt < m1; mt += kC8Warps) {
     const int x0 = mt * 16;
     auto row_ptr = [&](int x) {
@@ -655,7 +702,7 @@ cache8_attend_kernel(Attend8Args a) {
       for (int e = 0; e < 4; ++e) {
         s[nt][e] = x0 + lg + 8 * (e >> 1) < n_mem ? __fmul_rn(s[nt][e], a.scale_log2) : -INFINITY;
       }
-    st.step(s);
+    st.step(s, mem_ratio);
     uint32_t pb[NT][2][2];  // [part][row half]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -709,7 +756,7 @@ cache8_attend_kernel(Attend8Args a) {
         row[(D / 8) * lg + 2 * i + 1] = st.acc[nt][i][2 + h] * out;
       }
       if (lg == 0) {
-        row[D] = st.m[nt][h];
+        row[D] = st.m[nt][h] == kC8None ? -INFINITY : st.m[nt][h];
         row[D + 1] = L;
       }
     }

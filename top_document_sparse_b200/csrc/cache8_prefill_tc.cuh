@@ -499,7 +499,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     const int col = c0 + x * kC8tRows + r;
     const bool real = col < cols;
     const int vis = real ? column_rows(a, q, col) : 0;  // local rows the column sees
-    float m_run = -INFINITY, l_run = 0.0f, unit = kC8MinUnit;
+    float m_run = -INFINITY, l_run = 0.0f, unit = 0x1p-60f;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tmem_s = tmem + 128 * x + lane_base, tmem_o = tmem + kC8tTmemO + 128 * x + lane_base;
     bool okw = true;
