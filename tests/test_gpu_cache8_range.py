@@ -187,6 +187,27 @@ def test_attend_after_a_block_of_zeros(path, small):
     check_attend(mem, content, cache, Q.to(mem.dtype))
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("path", PATHS, ids=lambda p: "-".join(map(str, p)))
+@pytest.mark.parametrize("r", [12, 24, 25, 26, 60])
+def test_attend_blocks_of_16_rows_far_apart(path, fmt, r):
+    """Neighbouring blocks whose K and V scales are 2^r apart: K by a dimension that no query has, V
+    in rows of no weight."""
+    from top_document_sparse_b200 import msa
+    dt, D, T, G = path
+    mem, content = memory(torch_dtype(dt), 1, D)
+    kv, Q = rows_and_queries(dt, D, T, G, 160 + T, seed=r + D)
+    light(kv[0], slice(0, 16), D)
+    kv[1, :, :16] *= 2.0 ** r
+    kv[0, :, 48:64, :, 1] = 2.0 ** r
+    light(kv[0], slice(96, 112), D)
+    kv[1, :, 96:112] *= 2.0 ** r
+    kv[0, :, 96:112, :, 1] = 2.0 ** r
+    cache = msa.Cache8(mem, 1, 512, 16, fmt, track_weights=True)
+    cache.append(kv[0].to(mem.dtype), kv[1].to(mem.dtype))
+    check_attend(mem, content, cache, Q.to(mem.dtype))
+
+
 @pytest.mark.parametrize("path", PATHS, ids=lambda p: "-".join(map(str, p)))
 def test_attend_of_far_scores(path):
     """Scores of 2^16 to 2^110 where fp32 resolves no small difference: the row whose score is twice

@@ -8,10 +8,9 @@
 // softmax thread.  Both tiles share every context block of 64 rows:
 //   converters (warps 10-13) load a block's bytes, widen them to fp16 in
 //        registers and write them to shared memory in the MMA's layout, K and V
-//        each into a ring of four.  A block that spans several cache scales is
-//        brought to the largest of them by an exact power of two in the widening
-//        FMA, so one scale for K and one for V leave with the block.  bf16
-//        memory rows are brought to fp16 the same way, by a power of two that
+//        each into a ring of four.  Cached values are exact in fp16; their scales
+//        (one for K and one for V of every 16 rows) leave with the block for the
+//        softmax.  bf16 memory rows are brought to fp16 by a power of two that
 //        takes the block's largest element below 2.
 //   warps 8, 9  one for each tile: a thread issues S = Q K^T (M 128, N 64, K D; Q fp16, scaled by a
 //        power of two per column) into one of two TMEM buffers a tile, and
@@ -69,8 +68,9 @@ struct C8tSmem {
   static constexpr int kK = 2 * kQBytes;                // slots
   static constexpr int kV = kK + kC8tSlots * kKVBytes;
   static constexpr int kBars = kV + kC8tSlots * kKVBytes;
-  static constexpr int kScale = kBars + kCbN * 8;       // [block % (2 slots)][K, V]
-  static constexpr int kRed = kScale + 2 * kC8tSlots * 8;  // [converter warp]
+  static constexpr int kScales = 2 * kC8tBlk / 16;      // of 16 rows each, K's then V's
+  static constexpr int kScale = (kBars + kCbN * 8 + 15) / 16 * 16;  // [block % (2 slots)][kScales]
+  static constexpr int kRed = kScale + 2 * kC8tSlots * kScales * 4;  // [converter warp]
   static constexpr int kMisc = kRed + 16;               // TMEM slot, fail, memory rows
   static constexpr int kPre = kMisc + 16;
   static int bytes(int table_cap) { return 1024 + kPre + (2 * kMaxTopK + 1 + table_cap) * 4; }
@@ -116,27 +116,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr)
       : "memory");
-}
-
-// Four cached values as two fp16 pairs, times f (a power of two <= 1).
-template <int FMT>
-__device__ __forceinline__ uint2 widen4_scaled(uint32_t w, __half2 f, __half2 bias) {
-  uint32_t lo, hi;
-  if constexpr (FMT == MSA_CACHE_INT8) {
-    const uint32_t u = w ^ 0x80808080u;
-    const uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 a = __hfma2(*reinterpret_cast<const __half2 *>(&x), f, bias);  // (1152 + q) f - 1152 f
-    const __half2 b = __hfma2(*reinterpret_cast<const __half2 *>(&y), f, bias);
-    lo = *reinterpret_cast<const uint32_t *>(&a);
-    hi = *reinterpret_cast<const uint32_t *>(&b);
-  } else {
-    widen4<FMT>(w, lo, hi);
-    const __half2 a = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f);
-    const __half2 b = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f);
-    lo = *reinterpret_cast<const uint32_t *>(&a);
-    hi = *reinterpret_cast<const uint32_t *>(&b);
-  }
-  return make_uint2(lo, hi);
 }
 
 // The power of two at or below a finite x > 0, within the normal numbers that have a reciprocal.
@@ -313,9 +292,11 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         live = live && wait((h ? kCbFreeV0 : kCbFreeK0) + j % kC8tSlots, (j / kC8tSlots - 1) & 1);
       return live;
     };
-    // both scales of a block go out with K, so that S's barrier brings them to the softmax
-    auto put_scales = [&](int j, float k, float v) {
-      *reinterpret_cast<float2 *>(scales + 2 * (j % (2 * kC8tSlots))) = make_float2(k, v);
+    // a block's scales go out with K, so that S's barrier brings them to the softmax
+    auto put_scales = [&](int j, float4 k, float4 v) {
+      float4 *to = reinterpret_cast<float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)));
+      to[0] = k;
+      to[1] = v;
     };
     auto landed = [&](int j, int h) {
       fence_proxy_async_smem();  // the rows become visible to the tensor cores
@@ -326,8 +307,9 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     // are loaded a whole block ahead, right after the last ones left their registers.
     const int row0 = 2 * (tid >> 4) + ((tid >> 2) & 1), pc = 4 * ((tid >> 3) & 1) + (tid & 3);
     constexpr int N = kC8tBlk / 16;  // pieces of a half
+    static_assert(N == 4, "a float4 of scales");
     uint4 raw[2][N];
-    float rs[2][N];  // scales of the pieces' rows (0 past the last row)
+    float rs[2][N];  // thread 0: scales of 16 rows each (of the first ones past the last row)
     auto load_raw = [&](int u, int h) {
       if (u >= u1 || u >= lb) return;
       const uint8_t *src = (h ? a.v8 : a.k8) + (bh * a.cap + static_cast<int64_t>(u) * kC8tBlk + row0) * D + 16 * pc;
@@ -336,42 +318,34 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         raw[h][i] = make_uint4(0, 0, 0, 0);
-        rs[h][i] = 0.0f;
         if (left >= kC8tBlk || 16 * i + row0 < left) raw[h][i] = ld_stream16(src + 2048 * i);
-        if (16 * i < left) rs[h][i] = __ldg(sc + ((u * kC8tBlk + 16 * i) >> a.bl_shift));
+        if (tid == 0) rs[h][i] = __ldg(sc + ((u * kC8tBlk + (16 * i < left ? 16 * i : 0)) >> a.bl_shift));
       }
     };
     load_raw(u0, 0);
     load_raw(u0, 1);
     const int nl = max(0, min(u1, lb) - u0);  // local blocks of this split
     for (int j = 0; j < nl; ++j) {
-      float mx[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (h == 0) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mx[e] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) mx[e] = fmaxf(mx[e], rs[e][i]);
-            if (mx[e] == 0.0f) mx[e] = 1.0f;  // rows of zeros
-          }
-        }
-        const float inv = 1.0f / mx[h];  // a power of two
         if (!wait_slot(j, h)) continue;
-        if (h == 0 && tid == 0) put_scales(j, mx[0], mx[1]);
+        if (h == 0 && tid == 0) {
+          float top = fmaxf(fmaxf(rs[1][0], rs[1][1]), fmaxf(rs[1][2], rs[1][3]));
+          if (top == 0.0f) top = 1.0f;
+          auto v = [&](int i) { return rs[1][i] > 0.0f ? rs[1][i] : top; };  // (rows of zeros: any scale)
+          put_scales(j, make_float4(rs[0][0], rs[0][1], rs[0][2], rs[0][3]), make_float4(v(0), v(1), v(2), v(3)));
+        }
         uint8_t *dst = slot(j, h);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float f = rs[h][i] * inv;
-          const __half2 f2 = __float2half2_rn(f), bias = __float2half2_rn(-1152.0f * f);
           const uint4 x = raw[h][i];
-          const uint2 w0 = widen4_scaled<FMT>(x.x, f2, bias), w1 = widen4_scaled<FMT>(x.y, f2, bias);
-          const uint2 w2 = widen4_scaled<FMT>(x.z, f2, bias), w3 = widen4_scaled<FMT>(x.w, f2, bias);
-          *reinterpret_cast<uint4 *>(dst + ptc_swz(16 * i + row0, 2 * pc, kC8tBlk)) =
-              make_uint4(w0.x, w0.y, w1.x, w1.y);
-          *reinterpret_cast<uint4 *>(dst + ptc_swz(16 * i + row0, 2 * pc + 1, kC8tBlk)) =
-              make_uint4(w2.x, w2.y, w3.x, w3.y);
+          uint4 lo, hi;
+          widen4<FMT>(x.x, lo.x, lo.y);
+          widen4<FMT>(x.y, lo.z, lo.w);
+          widen4<FMT>(x.z, hi.x, hi.y);
+          widen4<FMT>(x.w, hi.z, hi.w);
+          *reinterpret_cast<uint4 *>(dst + ptc_swz(16 * i + row0, 2 * pc, kC8tBlk)) = lo;
+          *reinterpret_cast<uint4 *>(dst + ptc_swz(16 * i + row0, 2 * pc + 1, kC8tBlk)) = hi;
         }
         load_raw(u0 + j + 1, h);
         landed(j, h);
@@ -420,7 +394,8 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       for (int h = 0; h < 2; ++h) {  // w holds K
         if (h == 1) load(1);
         if (!wait_slot(j, h)) continue;
-        if (h == 0 && tid == 0) put_scales(j, mx[0], mx[1]);
+        if (h == 0 && tid == 0)
+          put_scales(j, make_float4(mx[0], mx[0], mx[0], mx[0]), make_float4(mx[1], mx[1], mx[1], mx[1]));
         const float inv = 1.0f / mx[h];
 #pragma unroll
         for (int i = 0; i < M; ++i) {
@@ -508,13 +483,16 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       okw = __all_sync(0xffffffffu, wait(kCbS0 + 2 * x + (j & 1), (j >> 1) & 1));
       if (!okw) break;
       tc05_fence_after();
-      // (positive even where the product underflows, so that a hidden row stays at -inf)
-      const float2 kv_scale = *reinterpret_cast<const float2 *>(scales + 2 * (j % (2 * kC8tSlots)));
-      float c = fmaxf(cf * kv_scale.x, 1.2e-38f);
-      const float v_scale = kv_scale.y;
-      const float unit_new = fmaxf(unit, v_scale);
-      // whole power of two: V's scale over the unit
-      const int lr = (__float_as_int(v_scale) >> 23) - (__float_as_int(unit_new) >> 23);
+      const float4 ks = *reinterpret_cast<const float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)));
+      const float4 vs = *reinterpret_cast<const float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)) + 4);
+      // score factors of 16 rows each (positive even where the product underflows, so that a hidden
+      // row stays at -inf)
+      float c[4] = {fmaxf(cf * ks.x, 1.2e-38f), fmaxf(cf * ks.y, 1.2e-38f), fmaxf(cf * ks.z, 1.2e-38f),
+                    fmaxf(cf * ks.w, 1.2e-38f)};
+      const float unit_new = fmaxf(fmaxf(unit, fmaxf(vs.x, vs.y)), fmaxf(vs.z, vs.w));
+      // log2 of V's scales over the unit, whole numbers
+      auto ratio_of = [&](float v) { return exponent_of(v) - exponent_of(unit_new); };
+      const float r[4] = {ratio_of(vs.x), ratio_of(vs.y), ratio_of(vs.z), ratio_of(vs.w)};
       const int lim = u < lb ? vis - u * kC8tBlk : real ? n_mem - (u - lb) * kC8tBlk : 0;  // rows seen
       const uint32_t at = tmem_s + kC8tBlk * (j & 1);
       float s[kC8tBlk];
@@ -524,12 +502,16 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
 #pragma unroll
         for (int i = 0; i < kC8tBlk; ++i) s[i] = i < lim ? s[i] : -INFINITY;
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float bm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kC8tBlk; i += 8)
+      for (int g = 0; g < 4; ++g) {
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
-      const float bm = __fmul_rn(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c);
+        for (int i = 16 * g; i < 16 * g + 16; i += 4)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
+        bm = fmaxf(bm, __fmul_rn(fmaxf(mx[0], mx[1]), c[g]));
+      }
       const float m_new = bm - m_run > kC8Slack ? bm + kC8Lead : m_run;  // (-inf - -inf: no)
       float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
       float ref = m_new == -INFINITY ? 0.0f : m_new;
@@ -537,13 +519,12 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         // far scores: the reference came from a rounded product, so the others are rounded alike, and
         // it leaves them before small terms are added that their rounding would swallow
 #pragma unroll
-        for (int i = 0; i < kC8tBlk; ++i) s[i] = __fmul_rn(s[i], c) - ref;
-        c = 1.0f;
+        for (int i = 0; i < kC8tBlk; ++i) s[i] = __fmul_rn(s[i], c[i / 16]) - ref;
+        c[0] = c[1] = c[2] = c[3] = 1.0f;
         ref = 0.0f;
       }
-      // the ratio of the scales in the exponent, unless it would take weights out of range
-      const bool fold = lr >= -24;
-      const float mf = ref - kC8Shift - (fold ? static_cast<float>(lr) : 0.0f);
+      // the ratios of the scales in the exponent, unless they would take weights out of range
+      const bool fold = fminf(fminf(r[0], r[1]), fminf(r[2], r[3])) >= -24.0f;
       l_run *= alpha;
       alpha *= unit / unit_new;
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
@@ -561,25 +542,29 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
           tmem_st32(tmem_o + cc, o);
         }
       }
-      float2 ps[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kC8tBlk; i += 2) {
-        const float2 e = fma2(make_float2(s[i], s[i + 1]), make_float2(c, c), make_float2(-mf, -mf));
-        s[i] = ex2_approx(e.x);
-        s[i + 1] = ex2_approx(e.y);
-        ps[(i >> 1) & 1] = add2(ps[(i >> 1) & 1], make_float2(s[i], s[i + 1]));
+      for (int g = 0; g < 4; ++g) {
+        const float rg = fold ? r[g] : 0.0f, mf = ref - kC8Shift - rg;
+        float2 ps = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+          const float2 e = fma2(make_float2(s[i], s[i + 1]), make_float2(c[g], c[g]), make_float2(-mf, -mf));
+          s[i] = ex2_approx(e.x);
+          s[i + 1] = ex2_approx(e.y);
+          ps = add2(ps, make_float2(s[i], s[i + 1]));
+        }
+        sum = fmaf(ps.x + ps.y, pow2_whole(-rg), sum);
       }
       if (!fold) {
-        const float ratio = v_scale / unit_new;
 #pragma unroll
-        for (int i = 0; i < kC8tBlk; ++i) s[i] *= ratio;
+        for (int i = 0; i < kC8tBlk; ++i) s[i] *= pow2_whole(fmaxf(r[i / 16], -127.0f));
       }
       uint32_t w[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) w[i] = pack_f16x2(s[2 * i], s[2 * i + 1]);
       tmem_st32(at, w);  // P over S
-      const float sum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
-      l_run += fold ? sum * __int_as_float((127 - lr) << 23) : sum;
+      l_run += sum;
       m_run = m_new;
       unit = unit_new;
       tc05_fence_before();
