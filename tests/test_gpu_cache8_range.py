@@ -239,3 +239,33 @@ def test_attend_of_far_scores(path):
             w[win] = 0.0
             assert torch.all(w == 0), (e, f)
     assert msa.device_error() == 0
+
+
+@pytest.mark.parametrize("path", PATHS, ids=lambda p: "-".join(map(str, p)))
+@pytest.mark.parametrize("r", [1, 3, 10])
+def test_attend_of_far_scores_in_smaller_blocks(path, r):
+    """The same where V of the row that takes all the weight is 2^r below the other blocks', which its
+    warp has met before it."""
+    from top_document_sparse_b200 import msa
+    dt, D, T, G = path
+    mem, content = memory(torch_dtype(dt), 1, D)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n, win = 8192, 77
+    K = torch.zeros(1, n, 1, D, device="cuda")
+    K[..., 0] = 0.5
+    K[:, win, :, 0] = 1.0
+    V = torch.randn(1, n, 1, D, generator=g, device="cuda") * 2.0 ** r
+    V[:, 64:80] *= 2.0 ** -r
+    cache = msa.Cache8(mem, 1, n, 16, "int8")
+    cache.append(K.to(mem.dtype), V.to(mem.dtype))
+    want = cache.read(None, n)[1][0, win].double()
+    ws = msa.workspace(cache.attend_workspace_size(T, 0, G))
+    for e in list(range(16, 40)) + [64, 110]:
+        for f in (1.0, 1.375, 1.75):
+            Q = torch.zeros(1, T, G, D, dtype=mem.dtype, device="cuda")
+            Q[..., 0] = f * 2.0 ** e
+            O = torch.empty_like(Q)
+            cache.attend(None, None, Q, O, ws)
+            err = (O.double() - want).abs()
+            assert torch.all(err <= 2.0 ** -8 * want.abs() if dt == "bf16" else err <= 2.0 ** -20 * want.abs()), (e, f)
+    assert msa.device_error() == 0

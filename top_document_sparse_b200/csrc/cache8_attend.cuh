@@ -317,10 +317,10 @@ __device__ __forceinline__ float exponent_of(float x) {
 __device__ __forceinline__ float scale_ratio(float scale, float unit) {
   return scale > 0.0f ? fmaxf(exponent_of(scale) - exponent_of(unit), kC8MinRatio) : kC8MinRatio;
 }
-// A reference 7 to 8 above the largest s + r.  Scores so large that their rounding swallows r: no lower
-// than that (P stays in fp16, and loses bits where r is not 0).
+// A reference 7 to 8 above the largest s + r.  Scores whose rounding swallows such sums: the score
+// itself (P is then 2^(r + 11) there).
 __device__ __forceinline__ float new_reference(float top, float r) {
-  return r == 0.0f ? ceilf(top) + kC8Lead : __fadd_ru(ceilf(top), r + kC8Lead);
+  return fabsf(top) < 8388608.0f ? ceilf(top) + (r + kC8Lead) : top;
 }
 // The unit grows by 2^up: how far the reference of a column with the sum l falls with it; the rest is
 // O's to lose.  (m is a whole number; where it is too large to fall, and before anything was seen, 0.)
