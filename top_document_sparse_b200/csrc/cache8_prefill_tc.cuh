@@ -18,14 +18,13 @@
 //        warp for both tiles was bound by the issue: 72 cycles an MMA, 113 a
 //        commit, 120 a barrier test)
 //   warps 0-3, 4-7  the softmax of a tile, a thread a column: S from TMEM, the
-//        hidden rows masked, P = 2^11 2^(s - m) times V's scale over the unit of
-//        O, written as fp16 over S: P is the MMA's A operand straight from TMEM,
+//        hidden rows masked, P = 2^(s - m + r + 11) (r: log2 of V's scale over the unit of
+//        O, as in cache8_attend.cuh), written as fp16 over S: P is the MMA's A operand straight from TMEM,
 //        so nothing but Q, K and V passes through shared memory.  The softmax of
 //        a block waits for no P V: the next S is ready when it ends, and only a
-//        move of the reference m (when a score passes it by 4 in log2 units; to 4
-//        above the score) waits for O's last update and rescales O's lane.  The
-//        ratio of V's scale to the unit is a whole power of two and goes into the
-//        exponent; the sum of a block's weights is brought back by the same power.
+//        move of the reference m (when s + r passes it by 4 in log2 units; to 7 to 8
+//        above) waits for O's last update and rescales O's lane.  r is a whole number
+//        and goes into the exponent; the sum of the weights of 16 rows is brought back by 2^-r.
 // 512 tokens x 32 heads over 8,704 + 128 rows: 166 us with P through shared
 // memory, 153 with blocks of 128 rows and one S a tile (S, softmax and P V of a
 // tile then follow one another).
@@ -43,6 +42,7 @@ constexpr int kC8tThreads = 32 * 10 + kC8tConv;
 constexpr int kC8tBlk = 64;                         // context rows per block
 constexpr int kC8tSlots = 4;                        // ring of K, ring of V
 constexpr int kC8tRows = 128;                       // columns per tile (UMMA M)
+constexpr float kC8MinFold = -40.0f;                // V scale ratios (log2) that go into P's exponent
 constexpr float kC8tFar = 2048.0f;                  // scores (log2 units) beyond this are "far"
 constexpr uint32_t kC8tTmemCols = 512;              // S, then P, of tile x at 128 x + 64 (block % 2),
 constexpr uint32_t kC8tTmemO = 256;                 // O of tile x at 256 + 128 x
@@ -68,7 +68,8 @@ struct C8tSmem {
   static constexpr int kK = 2 * kQBytes;                // slots
   static constexpr int kV = kK + kC8tSlots * kKVBytes;
   static constexpr int kBars = kV + kC8tSlots * kKVBytes;
-  static constexpr int kScales = 2 * kC8tBlk / 16;      // of 16 rows each, K's then V's
+  // K's scales of 16 rows each, log2 of V's over the unit (r), {log2 of the unit's growth, the unit, least r}
+  static constexpr int kScales = 12;
   static constexpr int kScale = (kBars + kCbN * 8 + 15) / 16 * 16;  // [block % (2 slots)][kScales]
   static constexpr int kRed = kScale + 2 * kC8tSlots * kScales * 4;  // [converter warp]
   static constexpr int kMisc = kRed + 16;               // TMEM slot, fail, memory rows
@@ -293,10 +294,17 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       return live;
     };
     // a block's scales go out with K, so that S's barrier brings them to the softmax
+    float unit = 0.0f;  // thread 0: the largest V scale so far
     auto put_scales = [&](int j, float4 k, float4 v) {
+      const float top = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+      const float up = top > unit && unit > 0.0f ? exponent_of(top) - exponent_of(unit) : 0.0f;
+      unit = fmaxf(unit, top);
+      auto ratio = [&](float x) { return x > 0.0f ? exponent_of(x) - exponent_of(unit) : kC8MinRatio; };  // (zeros)
+      const float4 r = make_float4(ratio(v.x), ratio(v.y), ratio(v.z), ratio(v.w));
       float4 *to = reinterpret_cast<float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)));
       to[0] = k;
-      to[1] = v;
+      to[1] = r;
+      to[2] = make_float4(up, unit, fminf(fminf(r.x, r.y), fminf(r.z, r.w)), 0.0f);
     };
     auto landed = [&](int j, int h) {
       fence_proxy_async_smem();  // the rows become visible to the tensor cores
@@ -329,12 +337,9 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!wait_slot(j, h)) continue;
-        if (h == 0 && tid == 0) {
-          float top = fmaxf(fmaxf(rs[1][0], rs[1][1]), fmaxf(rs[1][2], rs[1][3]));
-          if (top == 0.0f) top = 1.0f;
-          auto v = [&](int i) { return rs[1][i] > 0.0f ? rs[1][i] : top; };  // (rows of zeros: any scale)
-          put_scales(j, make_float4(rs[0][0], rs[0][1], rs[0][2], rs[0][3]), make_float4(v(0), v(1), v(2), v(3)));
-        }
+        if (h == 0 && tid == 0)
+          put_scales(j, make_float4(rs[0][0], rs[0][1], rs[0][2], rs[0][3]),
+                     make_float4(rs[1][0], rs[1][1], rs[1][2], rs[1][3]));
         uint8_t *dst = slot(j, h);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -388,7 +393,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         if (lane == 0) red[warp - 10] = top;
         asm volatile("bar.sync 1, %0;" ::"n"(kC8tConv) : "memory");
         top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        mx[h] = top > 0.0f ? floor_pow2(top) : 1.0f;
+        mx[h] = top > 0.0f ? floor_pow2(top) : 0.0f;
       }
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {  // w holds K
@@ -396,7 +401,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         if (!wait_slot(j, h)) continue;
         if (h == 0 && tid == 0)
           put_scales(j, make_float4(mx[0], mx[0], mx[0], mx[0]), make_float4(mx[1], mx[1], mx[1], mx[1]));
-        const float inv = 1.0f / mx[h];
+        const float inv = mx[h] > 0.0f ? 1.0f / mx[h] : 1.0f;
 #pragma unroll
         for (int i = 0; i < M; ++i) {
           const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -474,7 +479,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     const int col = c0 + x * kC8tRows + r;
     const bool real = col < cols;
     const int vis = real ? column_rows(a, q, col) : 0;  // local rows the column sees
-    float m_run = -INFINITY, l_run = 0.0f, unit = 0x1p-60f;
+    float m_run = kC8None, l_run = 0.0f, unit = 0.0f;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tmem_s = tmem + 128 * x + lane_base, tmem_o = tmem + kC8tTmemO + 128 * x + lane_base;
     bool okw = true;
@@ -483,16 +488,21 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       okw = __all_sync(0xffffffffu, wait(kCbS0 + 2 * x + (j & 1), (j >> 1) & 1));
       if (!okw) break;
       tc05_fence_after();
-      const float4 ks = *reinterpret_cast<const float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)));
-      const float4 vs = *reinterpret_cast<const float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)) + 4);
+      const float4 *sc = reinterpret_cast<const float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)));
+      const float4 ks = sc[0], rs = sc[1], us = sc[2];
       // score factors of 16 rows each (positive even where the product underflows, so that a hidden
       // row stays at -inf)
       float c[4] = {fmaxf(cf * ks.x, 1.2e-38f), fmaxf(cf * ks.y, 1.2e-38f), fmaxf(cf * ks.z, 1.2e-38f),
                     fmaxf(cf * ks.w, 1.2e-38f)};
-      const float unit_new = fmaxf(fmaxf(unit, fmaxf(vs.x, vs.y)), fmaxf(vs.z, vs.w));
-      // log2 of V's scales over the unit, whole numbers
-      auto ratio_of = [&](float v) { return exponent_of(v) - exponent_of(unit_new); };
-      const float r[4] = {ratio_of(vs.x), ratio_of(vs.y), ratio_of(vs.z), ratio_of(vs.w)};
+      const float r[4] = {rs.x, rs.y, rs.z, rs.w};
+      float alpha = 1.0f;  // factor of O's lane
+      if (us.x > 0.0f) {   // a larger unit: the reference falls as in Softmax8
+        const float k = reference_falls(m_run, l_run, us.x);
+        m_run -= k;
+        l_run *= pow2_whole(k);
+        alpha = pow2_whole(fmaxf(k - us.x, -127.0f));
+      }
+      unit = us.y;
       const int lim = u < lb ? vis - u * kC8tBlk : real ? n_mem - (u - lb) * kC8tBlk : 0;  // rows seen
       const uint32_t at = tmem_s + kC8tBlk * (j & 1);
       float s[kC8tBlk];
@@ -502,7 +512,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
 #pragma unroll
         for (int i = 0; i < kC8tBlk; ++i) s[i] = i < lim ? s[i] : -INFINITY;
       }
-      float bm = -INFINITY;
+      float top[4], over = -INFINITY;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float mx[2] = {-INFINITY, -INFINITY};
@@ -510,11 +520,19 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         for (int i = 16 * g; i < 16 * g + 16; i += 4)
 #pragma unroll
           for (int e = 0; e < 2; ++e) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
-        bm = fmaxf(bm, __fmul_rn(fmaxf(mx[0], mx[1]), c[g]));
+        top[g] = __fmul_rn(fmaxf(mx[0], mx[1]), c[g]);
+        over = fmaxf(over, top[g] - m_run + fmaxf(r[g], kC8MinRatio));
       }
-      const float m_new = bm - m_run > kC8Slack ? bm + kC8Lead : m_run;  // (-inf - -inf: no)
-      float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
-      float ref = m_new == -INFINITY ? 0.0f : m_new;
+      if (over > kC8Slack) {
+        float m_new = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) m_new = fmaxf(m_new, new_reference(top[g], fmaxf(r[g], kC8MinRatio)));
+        const float f = ex2_approx(m_run - m_new);
+        m_run = m_new;
+        l_run *= f;
+        alpha *= f;
+      }
+      float ref = m_run;
       if (fabsf(ref) > kC8tFar) {
         // far scores: the reference came from a rounded product, so the others are rounded alike, and
         // it leaves them before small terms are added that their rounding would swallow
@@ -524,9 +542,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         ref = 0.0f;
       }
       // the ratios of the scales in the exponent, unless they would take weights out of range
-      const bool fold = fminf(fminf(r[0], r[1]), fminf(r[2], r[3])) >= -24.0f;
-      l_run *= alpha;
-      alpha *= unit / unit_new;
+      const bool fold = us.z >= kC8MinFold;
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
         // O's lane follows the reference and the unit, once the last P V has completed (TMEM
         // accesses are warp-collective)
@@ -565,8 +581,6 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       for (int i = 0; i < 32; ++i) w[i] = pack_f16x2(s[2 * i], s[2 * i + 1]);
       tmem_st32(at, w);  // P over S
       l_run += sum;
-      m_run = m_new;
-      unit = unit_new;
       tc05_fence_before();
       mbar_arrive(bar(kCbP0 + 2 * x + (j & 1)));
     }
@@ -629,7 +643,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       if (one) {
         write_stats(a, row, m_run, l);
       } else {
-        a.part_ml[(static_cast<int64_t>(row) * a.n_split + split) * 2] = m_run;
+        a.part_ml[(static_cast<int64_t>(row) * a.n_split + split) * 2] = m_run == kC8None ? -INFINITY : m_run;
         a.part_ml[(static_cast<int64_t>(row) * a.n_split + split) * 2 + 1] = l;
       }
     }
