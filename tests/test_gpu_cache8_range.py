@@ -42,22 +42,22 @@ QMAX = {"int8": 127.0, "e4m3": 448.0}
 def expected(ref, mem_rows, Q, n, bf16):
     """O, lse, weights and their bounds in fp64.  First order in u = 2^-23, for each column by itself:
       ds_j = (D + 17) u sum_d |q_d k_jd| / sqrt(D)  (sums on the tensor cores may truncate)
-             + sum_d (lost(q_d) |k_jd| + [memory row] lost(k_jd) |q_d|) / sqrt(D)
+             + sum_d (lost(q_d) |k_jd| + [memory row] 2^6 lost(k_jd) |q_d|) / sqrt(D)
       lost : 2^-25 of a row's largest element for elements whose bits reach below fp16's smallest
-             step there: bf16's 8 bits below 2^-16 of the largest, fp32's all (zeros lose nothing)
+             step there: bf16's 8 bits below 2^-16 of the largest, fp32's all (zeros lose nothing);
+             a memory row of K shares a power of two with rows up to 2^6 larger
       dl   = sum_j p_j ds_j + (rows + 8) u                        of the log-sum
       O    : sum_j p_j |v_j| (ds_j + dl + w + (rows + 16) u), w the rounding of a weight: 2^-11 to
              fp16 (bf16 queries), 2^-22 to its head and tail (fp32)
              + 2^-28 P sum_j |v_j| / s_j: weights below fp16's normal range, half its smallest step
              2^-25 against weights times scales kept at 2^11 2^-8 of P = max_j p_j s_j or above
-             + 2^-25 sum_(memory rows) p_j max|v_j|                a bf16 row as fp16
-    A scale s_j of a memory row is the power of two at or below its largest element.  A block or a
-    row of little weight enters by that weight alone, however large its values are."""
+    (memory rows: V and a weight's head and tail are bf16, nothing is below their normal range).
+    A block or a row of little weight enters by that weight alone, however large its values are."""
     B, T, Hq, D = Q.shape
 
-    def lost(x):
+    def lost(x, below=1.0):
         a = np.abs(x)
-        top = a.max(-1, initial=0.0, keepdims=True)
+        top = below * a.max(-1, initial=0.0, keepdims=True)
         return np.where((a > 0) & ((a < 2.0 ** -16 * top) | (not bf16)), 2.0 ** -25 * top, 0.0)
 
     G, w = Hq // ref.H, 2.0 ** -11 if bf16 else 2.0 ** -22
@@ -70,11 +70,9 @@ def expected(ref, mem_rows, Q, n, bf16):
             M = mem_rows[b][0].shape[0]
             K = np.concatenate([mem_rows[b][0][:, g], ref.values(b, g, "k")])
             V = np.concatenate([mem_rows[b][1][:, g], ref.values(b, g, "v")])
-            top = np.abs(V[:M]).max(1, initial=0.0)
-            s = np.concatenate([2.0 ** np.floor(np.log2(np.maximum(top, 1e-30))),
-                                np.repeat(ref.vs[b, g], ref.bl)[:ln]])
+            s = np.concatenate([np.zeros(M), np.repeat(ref.vs[b, g], ref.bl)[:ln]])
             vq = np.where(s[:, None] > 0, np.abs(V) / np.where(s > 0, s, 1.0)[:, None], 0.0)
-            kl = np.concatenate([lost(K[:M]), np.zeros((ln, D))])
+            kl = np.concatenate([lost(K[:M], 64.0), np.zeros((ln, D))])
             for t in range(int(n[b])):
                 seen = M + max(0, ln - int(n[b]) + t + 1)
                 rows = seen
@@ -93,8 +91,7 @@ def expected(ref, mem_rows, Q, n, bf16):
                     a = np.abs(V[:seen])
                     O[b, t, h] = p @ V[:seen]
                     tol[b, t, h] = ((p * (ds + dl + w + (rows + 16) * U)) @ a
-                                    + 2.0 ** -28 * (p * s[:seen]).max() * vq[:seen].sum(0)
-                                    + 2.0 ** -25 * (p[:M] @ top))
+                                    + 2.0 ** -28 * (p * s[:seen]).max() * vq[:seen].sum(0))
                     tl[b, t, h] = dl + 4 * U * abs(lse[b, t, h])
                     W[b, g, :seen - M] += p[M:]
                     tw[b, g, :seen - M] += p[M:] * (ds[M:] + tl[b, t, h] + 16 * U)
@@ -203,6 +200,28 @@ def test_attend_blocks_of_16_rows_far_apart(path, fmt, r):
     cache = msa.Cache8(mem, 1, 512, 16, fmt, track_weights=True)
     cache.append(kv[0].to(mem.dtype), kv[1].to(mem.dtype))
     check_attend(mem, content, cache, Q.to(mem.dtype))
+
+
+@pytest.mark.parametrize("path", PATHS, ids=lambda p: "-".join(map(str, p)))
+@pytest.mark.parametrize("r", [0, 12, 24, 60])
+def test_attend_memory_rows_far_apart(path, r):
+    """One memory row with V 2^r times the others' and no weight, one with K 2^r larger in a
+    dimension that no query has, rows of zeros; few and tiny local rows."""
+    from top_document_sparse_b200 import msa
+    dt, D, T, G = path
+    mem, content = memory(torch_dtype(dt), 1, D, docs=(64 * 40, 64 * 3))
+    kv, Q = rows_and_queries(dt, D, T, G, mem.n_chunks, seed=r)
+    kv = kv[:, 0]
+    light(kv[0][None], slice(3, 4), D)
+    kv[1, 3] *= 2.0 ** r
+    kv[0, 7, :, 1] = 2.0 ** r
+    kv[:, 11] = 0.0
+    content.copy_(kv.transpose(0, 1).to(mem.dtype))
+    cache = msa.Cache8(mem, 1, 256, 16, "int8")
+    loc = torch.randn(2, 1, T, 1, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    cache.append(loc[0].to(mem.dtype), (loc[1] * 2.0 ** -r).to(mem.dtype))
+    ids = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    check_attend(mem, content, cache, Q.to(mem.dtype), ids)
 
 
 @pytest.mark.parametrize("path", PATHS, ids=lambda p: "-".join(map(str, p)))

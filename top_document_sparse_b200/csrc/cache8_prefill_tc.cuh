@@ -10,8 +10,12 @@
 //        registers and write them to shared memory in the MMA's layout, K and V
 //        each into a ring of four.  Cached values are exact in fp16; their scales
 //        (one for K and one for V of every 16 rows) leave with the block for the
-//        softmax.  bf16 memory rows are brought to fp16 by a power of two that
-//        takes the block's largest element below 2.
+//        softmax.  K of bf16 memory rows is brought to fp16 by a power of two that
+//        takes the block's largest element below 2, or, where a row lies 2^6 and more below
+//        another, by one of its own for every row, which leaves with the block (elements
+//        below 2^-10 of their row's largest may lose bits, 2^-19 of it at most).  Their V stays
+//        bf16, P is then a bf16 head and tail and P V two MMAs.  So a row costs the others
+//        nothing, however large it is.
 //   warps 8, 9  one for each tile: a thread issues S = Q K^T (M 128, N 64, K D; Q fp16, scaled by a
 //        power of two per column) into one of two TMEM buffers a tile, and
 //        O += P V (M 128, N D, K 64), each as soon as its inputs are ready (one
@@ -68,11 +72,13 @@ struct C8tSmem {
   static constexpr int kK = 2 * kQBytes;                // slots
   static constexpr int kV = kK + kC8tSlots * kKVBytes;
   static constexpr int kBars = kV + kC8tSlots * kKVBytes;
-  // K's scales of 16 rows each, log2 of V's over the unit (r), {log2 of the unit's growth, the unit, least r}
+  // K's scales of 16 rows each, log2 of V's over the unit (r), {log2 of the unit's growth, the unit,
+  // least r, whether the rows of K have scales of their own}
   static constexpr int kScales = 12;
   static constexpr int kScale = (kBars + kCbN * 8 + 15) / 16 * 16;  // [block % (2 slots)][kScales]
-  static constexpr int kRed = kScale + 2 * kC8tSlots * kScales * 4;  // [converter warp]
-  static constexpr int kMisc = kRed + 16;               // TMEM slot, fail, memory rows
+  static constexpr int kRowScale = kScale + 2 * kC8tSlots * kScales * 4;  // [block % (2 slots)][row]
+  static constexpr int kRed = kRowScale + 2 * kC8tSlots * kC8tBlk * 4;    // [converter warp]
+  static constexpr int kMisc = kRed + 32;               // TMEM slot, fail, memory rows
   static constexpr int kPre = kMisc + 16;
   static int bytes(int table_cap) { return 1024 + kPre + (2 * kMaxTopK + 1 + table_cap) * 4; }
 };
@@ -158,7 +164,8 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Sm::kBars);
   float *scales = reinterpret_cast<float *>(sm + Sm::kScale);
-  float *red = reinterpret_cast<float *>(sm + Sm::kRed);
+  auto row_scales = [&](int j) { return reinterpret_cast<float *>(sm + Sm::kRowScale) + kC8tBlk * (j % (2 * kC8tSlots)); };
+  float2 *red = reinterpret_cast<float2 *>(sm + Sm::kRed);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Sm::kMisc);
   volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *mem_rows = reinterpret_cast<int *>(tmem_slot + 2);
@@ -295,7 +302,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     };
     // a block's scales go out with K, so that S's barrier brings them to the softmax
     float unit = 0.0f;  // thread 0: the largest V scale so far
-    auto put_scales = [&](int j, float4 k, float4 v) {
+    auto put_scales = [&](int j, float4 k, float4 v, bool rows) {
       const float top = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
       const float up = top > unit && unit > 0.0f ? exponent_of(top) - exponent_of(unit) : 0.0f;
       unit = fmaxf(unit, top);
@@ -304,7 +311,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       float4 *to = reinterpret_cast<float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)));
       to[0] = k;
       to[1] = r;
-      to[2] = make_float4(up, unit, fminf(fminf(r.x, r.y), fminf(r.z, r.w)), 0.0f);
+      to[2] = make_float4(up, unit, fminf(fminf(r.x, r.y), fminf(r.z, r.w)), rows ? 1.0f : 0.0f);
     };
     auto landed = [&](int j, int h) {
       fence_proxy_async_smem();  // the rows become visible to the tensor cores
@@ -339,7 +346,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         if (!wait_slot(j, h)) continue;
         if (h == 0 && tid == 0)
           put_scales(j, make_float4(rs[0][0], rs[0][1], rs[0][2], rs[0][3]),
-                     make_float4(rs[1][0], rs[1][1], rs[1][2], rs[1][3]));
+                     make_float4(rs[1][0], rs[1][1], rs[1][2], rs[1][3]), false);
         uint8_t *dst = slot(j, h);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -356,8 +363,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         landed(j, h);
       }
     }
-    // memory rows, bf16: pieces of 8 elements, 16 a row; V's largest element is found before K goes
-    // out, V being read a second time for its conversion
+    // memory rows, bf16: pieces of 8 elements, 16 a row; V as it is
     const int64_t kv = static_cast<int64_t>(a.H_kv) * D;
     constexpr int M = kC8tBlk / 8;
     if (nblk > nl) {
@@ -366,10 +372,9 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     }
     for (int j = nl; j < nblk; ++j) {
       uint4 w[M];
-      float mx[2];
+      const int x0 = (u0 + j - lb) * kC8tBlk + (tid >> 4);
       auto load = [&](int h) {
         const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.content) + h * kv + g * D + 8 * (tid & 15);
-        const int x0 = (u0 + j - lb) * kC8tBlk + (tid >> 4);
 #pragma unroll
         for (int i = 0; i < M; ++i) {
           const int x = x0 + 8 * i;
@@ -377,42 +382,69 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
           if (x < n_mem) w[i] = *reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(table[x]) * 2 * kv);
         }
       };
-#pragma unroll 1
-      for (int h = 1; h >= 0; --h) {
-        load(h);
-        float top = 0.0f;
+      auto largest = [&](uint4 x) {
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-          const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        for (int e = 0; e < 4; ++e)
+          m = max3(m, finite_abs(__uint_as_float(y[e] << 16)), finite_abs(__uint_as_float(y[e] & 0xffff0000u)));
+        return m;
+      };
+      auto put = [&](int h, int i, uint4 x) {
+        *reinterpret_cast<uint4 *>(slot(j, h) + ptc_swz(8 * i + (tid >> 4), tid & 15, kC8tBlk)) = x;
+      };
+      auto put_k = [&](int i, float inv) {
+        const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t z[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top = max3(top, finite_abs(__uint_as_float(y[e] << 16)), finite_abs(__uint_as_float(y[e] & 0xffff0000u)));
-        }
-        top = warp_max(top);
-        asm volatile("bar.sync 1, %0;" ::"n"(kC8tConv) : "memory");  // `red` was read
-        if (lane == 0) red[warp - 10] = top;
-        asm volatile("bar.sync 1, %0;" ::"n"(kC8tConv) : "memory");
-        top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        mx[h] = top > 0.0f ? floor_pow2(top) : 0.0f;
+        for (int e = 0; e < 4; ++e)
+          z[e] = pack_f16x2(__uint_as_float(y[e] << 16) * inv, __uint_as_float(y[e] & 0xffff0000u) * inv);
+        put(0, i, make_uint4(z[0], z[1], z[2], z[3]));
+      };
+      load(0);
+      // the largest and the smallest of the block's pieces; a row far below another has small ones
+      float hi = 0.0f, lo = INFINITY;
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        const float m = largest(w[i]);
+        hi = fmaxf(hi, m);
+        if (x0 + 8 * i < n_mem) lo = fminf(lo, m);
       }
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {  // w holds K
-        if (h == 1) load(1);
-        if (!wait_slot(j, h)) continue;
-        if (h == 0 && tid == 0)
-          put_scales(j, make_float4(mx[0], mx[0], mx[0], mx[0]), make_float4(mx[1], mx[1], mx[1], mx[1]));
-        const float inv = mx[h] > 0.0f ? 1.0f / mx[h] : 1.0f;
+      hi = warp_max(hi);
+      lo = -warp_max(-lo);
+      asm volatile("bar.sync 1, %0;" ::"n"(kC8tConv) : "memory");  // `red` was read
+      if (lane == 0) red[warp - 10] = make_float2(hi, lo);
+      asm volatile("bar.sync 1, %0;" ::"n"(kC8tConv) : "memory");
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-          const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          uint32_t z[4];
+      for (int i = 0; i < kC8tConv / 32; ++i) {
+        hi = fmaxf(hi, red[i].x);
+        lo = fminf(lo, red[i].y);
+      }
+      const bool rows = lo < 0x1p-6f * hi;
+      if (wait_slot(j, 0)) {
+        const float k = rows || hi == 0.0f ? 1.0f : floor_pow2(hi);
+        if (tid == 0) put_scales(j, make_float4(k, k, k, k), make_float4(1.0f, 1.0f, 1.0f, 1.0f), rows);
+        if (rows) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            z[e] = pack_f16x2(__uint_as_float(y[e] << 16) * inv, __uint_as_float(y[e] & 0xffff0000u) * inv);
-          *reinterpret_cast<uint4 *>(slot(j, h) + ptc_swz(8 * i + (tid >> 4), tid & 15, kC8tBlk)) =
-              make_uint4(z[0], z[1], z[2], z[3]);
+          for (int i = 0; i < M; ++i) {
+            float m = largest(w[i]);  // of the row, which sixteen lanes share
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float own = m > 0.0f ? floor_pow2(m) : 1.0f;
+            if ((tid & 15) == 0) row_scales(j)[8 * i + (tid >> 4)] = own;
+            put_k(i, 1.0f / own);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < M; ++i) put_k(i, 1.0f / k);
         }
-        landed(j, h);
+        landed(j, 0);
+      }
+      load(1);
+      if (wait_slot(j, 1)) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) put(1, i, w[i]);
+        landed(j, 1);
       }
     }
   } else if (warp >= 8) {
@@ -421,6 +453,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     // lane 0 alone issues.
     constexpr uint32_t idesc_s = umma_idesc_f16_f32<kC8tRows, kC8tBlk>();
     constexpr uint32_t idesc_o = umma_idesc_f16_f32<kC8tRows, D>() | (1u << 16);  // B MN-major
+    constexpr uint32_t idesc_m = umma_idesc_bf16_f32_bmn<kC8tRows, D>();          // of memory rows
     const int x = warp - 8;
     const int n = x == 0 || act1 ? nblk : 0;
     // descriptors of the first slots; a step adds its offset in units of 16 bytes
@@ -458,9 +491,16 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       tc05_fence_after();
       const uint64_t vd = v_desc + static_cast<uint32_t>(s * (Sm::kKVBytes >> 4));
       if (lane == 0) {
+        const uint32_t pt = tmem + 128 * x + 64 * u;
+        if (u0 + j < lb) {
 #pragma unroll
-        for (int i = 0; i < kC8tBlk / 16; ++i)
-          umma_f16_ts(o, tmem + 128 * x + 64 * u + 8 * i, vd + i * 128, idesc_o, (j | i) != 0);
+          for (int i = 0; i < kC8tBlk / 16; ++i) umma_f16_ts(o, pt + 8 * i, vd + i * 128, idesc_o, (j | i) != 0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kC8tBlk / 16; ++i) umma_f16_ts(o, pt + 8 * i, vd + i * 128, idesc_m, (j | i) != 0);
+#pragma unroll
+          for (int i = 0; i < kC8tBlk / 16; ++i) umma_f16_ts(o, pt + 32 + 8 * i, vd + i * 128, idesc_m, 1);
+        }
         umma_commit(bar(kCbO0 + 2 * x + u));
         umma_commit(bar(kCbFreeV0 + s));
       }
@@ -489,6 +529,17 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       if (!okw) break;
       tc05_fence_after();
       const float4 *sc = reinterpret_cast<const float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)));
+      const uint32_t at = tmem_s + kC8tBlk * (j & 1);
+      if (u >= lb && sc[2].w != 0.0f) {  // memory rows of very different size (in place: no registers are kept for it)
+#pragma unroll 1
+        for (int i = 0; i < kC8tBlk; i += 16) {
+          float y[16];
+          tmem_ld16(at + i, y);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] *= row_scales(j)[i + e];
+          tmem_st16(at + i, y);
+        }
+      }
       const float4 ks = sc[0], rs = sc[1], us = sc[2];
       // score factors of 16 rows each (positive even where the product underflows, so that a hidden
       // row stays at -inf)
@@ -504,7 +555,6 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       }
       unit = us.y;
       const int lim = u < lb ? vis - u * kC8tBlk : real ? n_mem - (u - lb) * kC8tBlk : 0;  // rows seen
-      const uint32_t at = tmem_s + kC8tBlk * (j & 1);
       float s[kC8tBlk];
       static_assert(kC8tBlk == 64, "one 64-column TMEM load per block");
       tmem_ld64(at, s);
@@ -577,9 +627,22 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         for (int i = 0; i < kC8tBlk; ++i) s[i] *= pow2_whole(fmaxf(r[i / 16], -127.0f));
       }
       uint32_t w[32];
+      if (u >= lb) {  // memory rows: bf16, the tail behind the head
 #pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = pack_f16x2(s[2 * i], s[2 * i + 1]);
-      tmem_st32(at, w);  // P over S
+        for (int i = 0; i < 32; ++i) {
+          w[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
+          s[2 * i] -= __uint_as_float(w[i] << 16);
+          s[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+        }
+        tmem_st32(at, w);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
+        tmem_st32(at + 32, w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = pack_f16x2(s[2 * i], s[2 * i + 1]);
+        tmem_st32(at, w);  // P over S
+      }
       l_run += sum;
       tc05_fence_before();
       mbar_arrive(bar(kCbP0 + 2 * x + (j & 1)));
