@@ -166,3 +166,19 @@ def test_rope_on_another_stream_leaves_freed_blocks_alone():
     got, _ = rope.rotate(q, None, pos, stream=other)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.all(keep == 7.0)
+
+
+@pytest.mark.parametrize("original", [1, 4, 6, 7])
+def test_rope_yarn_of_short_original_lengths(original):
+    """Where no pair turns once within original_length (2 pi positions) every frequency is divided by
+    the factor, as in linear scaling; above it pair 0 keeps its own."""
+    from top_document_sparse_b200 import msa
+    x = torch.randn(9, 2, 64, device="cuda")
+    pos = torch.arange(9, device="cuda") * 1001
+    yarn, _ = msa.Rope(64, scaling="yarn", factor=4.0, original_length=original, magnitude=1.0).rotate(x, None, pos)
+    linear, _ = msa.Rope(64, scaling="linear", factor=4.0, magnitude=1.0).rotate(x, None, pos)
+    plain, _ = msa.Rope(64, magnitude=1.0).rotate(x, None, pos)
+    if original < 2 * math.pi:
+        assert torch.equal(yarn, linear)
+    else:
+        assert torch.equal(yarn[..., ::32], plain[..., ::32]) and torch.equal(yarn[..., 1::32], linear[..., 1::32])

@@ -99,7 +99,8 @@ msa_status rope_frequencies(const msa_rope_config *c, std::vector<uint64_t> &fre
     double f = std::pow(theta, -2.0 * i / r);
     if (c->scaling == MSA_ROPE_LINEAR) f /= c->factor;
     if (c->scaling == MSA_ROPE_YARN) {
-      const double ramp = std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
+      // (high <= 0: not even pair 0 turns once)
+      const double ramp = high <= 0.0 ? 1.0 : std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
       f = f / c->factor * ramp + f * (1.0 - ramp);
     }
     const long double turns = static_cast<long double>(f) / 6.283185307179586476925286766559L;
