@@ -141,3 +141,32 @@ def test_serving_calls_reject_null_handles():
 def test_attend_fetched_rejects_null_handles():
     assert msa.lib().msa_cache8_attend_fetched(None, None, None, 0, None, 1, 1, None, None, None, None,
                                                -1.0, None, 0, None) == 1
+
+
+def test_cache8_workspace_sizes_are_asked_on_the_caches_device(monkeypatch):
+    """The size calls answer 0 for a memory of another device than the current one; a cache asks with
+    its own device current, whatever the caller's is."""
+    import contextlib
+    import types
+
+    import torch
+
+    current, asked = ["cuda:0"], []
+
+    @contextlib.contextmanager
+    def device(d):
+        current.append(str(d))
+        yield
+        current.pop()
+
+    def size(*args):
+        asked.append(current[-1])
+        return 4096
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(msa, "_lib", types.SimpleNamespace(msa_cache8_attend_workspace_size=size,
+                                                           msa_cache8_evict_workspace_size=size))
+    cache = msa.Cache8.__new__(msa.Cache8)
+    cache.mem, cache._ref, cache.device = types.SimpleNamespace(handle=None), None, torch.device("cuda:1")
+    assert cache.attend_workspace_size(1, 4, 8) == 4096 and cache.evict_workspace_size() == 4096
+    assert asked == ["cuda:1", "cuda:1"] and current == ["cuda:0"]

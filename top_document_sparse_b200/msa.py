@@ -702,8 +702,9 @@ class Cache8:
         return K_out, V_out
 
     def attend_workspace_size(self, tokens: int, k: int, n_q_heads: int) -> int:
-        return _lib.msa_cache8_attend_workspace_size(self.mem.handle, self._ref, tokens, k,
-                                                     n_q_heads)
+        with torch.cuda.device(self.device):  # (the library sizes for the current device)
+            return _lib.msa_cache8_attend_workspace_size(self.mem.handle, self._ref, tokens, k,
+                                                         n_q_heads)
 
     def attend(self, content, ids, Q, O, workspace, lse=None, n_tokens=None, weight_decay=None,
                stream=None):
@@ -736,7 +737,8 @@ class Cache8:
               *_buffer(workspace, "workspace", dev))
 
     def evict_workspace_size(self) -> int:
-        return _lib.msa_cache8_evict_workspace_size(self.mem.handle, self._ref)
+        with torch.cuda.device(self.device):
+            return _lib.msa_cache8_evict_workspace_size(self.mem.handle, self._ref)
 
     def evict(self, budget: int, recent: int, workspace, out: "Cache8 | None" = None, stream=None):
         """Keep at most ``budget`` rows a query: whole blocks leave by their accumulated attention
