@@ -296,8 +296,8 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     // half h (0: K, 1: V) of the j-th block: its slot, waited for; false after a timeout
     auto slot = [&](int j, int h) { return sm + (h ? Sm::kV : Sm::kK) + (j % kC8tSlots) * Sm::kKVBytes; };
     auto wait_slot = [&](int j, int h) {
-      if (j >= kC8tSlots)
-        live = live && wait((h ? kCbFreeV0 : kCbFreeK0) + j % kC8tSlots, (j / kC8tSlots - 1) & 1);
+      if (j >= kC8tSlots)  // (the lanes of a warp agree: what follows may be warp-collective)
+        live = __all_sync(0xffffffffu, live && wait((h ? kCbFreeV0 : kCbFreeK0) + j % kC8tSlots, (j / kC8tSlots - 1) & 1));
       return live;
     };
     // a block's scales go out with K, so that S's barrier brings them to the softmax
