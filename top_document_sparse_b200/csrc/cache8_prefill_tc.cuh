@@ -522,15 +522,16 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     float m_run = kC8None, l_run = 0.0f, unit = 0.0f;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tmem_s = tmem + 128 * x + lane_base, tmem_o = tmem + kC8tTmemO + 128 * x + lane_base;
-    bool okw = true;
-    for (int j = 0; j < nblk; ++j) {
+    // block j; false after a timeout.  Local and memory blocks have code of their own: in one loop the
+    // memory blocks' branches cost the local ones 2%.
+    auto block = [&](int j, auto memory) -> bool {
+      constexpr bool kMem = decltype(memory)::value;
       const int u = u0 + j;
-      okw = __all_sync(0xffffffffu, wait(kCbS0 + 2 * x + (j & 1), (j >> 1) & 1));
-      if (!okw) break;
+      if (!__all_sync(0xffffffffu, wait(kCbS0 + 2 * x + (j & 1), (j >> 1) & 1))) return false;
       tc05_fence_after();
       const float4 *sc = reinterpret_cast<const float4 *>(scales + Sm::kScales * (j % (2 * kC8tSlots)));
       const uint32_t at = tmem_s + kC8tBlk * (j & 1);
-      if (u >= lb && sc[2].w != 0.0f) {  // memory rows of very different size (in place: no registers are kept for it)
+      if (kMem && sc[2].w != 0.0f) {  // memory rows of very different size
 #pragma unroll 1
         for (int i = 0; i < kC8tBlk; i += 16) {
           float y[16];
@@ -554,7 +555,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         alpha = pow2_whole(fmaxf(k - us.x, -127.0f));
       }
       unit = us.y;
-      const int lim = u < lb ? vis - u * kC8tBlk : real ? n_mem - (u - lb) * kC8tBlk : 0;  // rows seen
+      const int lim = !kMem ? vis - u * kC8tBlk : real ? n_mem - (u - lb) * kC8tBlk : 0;  // rows seen
       float s[kC8tBlk];
       static_assert(kC8tBlk == 64, "one 64-column TMEM load per block");
       tmem_ld64(at, s);
@@ -596,8 +597,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
         // O's lane follows the reference and the unit, once the last P V has completed (TMEM
         // accesses are warp-collective)
-        okw = __all_sync(0xffffffffu, wait(kCbO0 + 2 * x + ((j - 1) & 1), ((j - 1) >> 1) & 1));
-        if (!okw) break;
+        if (!__all_sync(0xffffffffu, wait(kCbO0 + 2 * x + ((j - 1) & 1), ((j - 1) >> 1) & 1))) return false;
         tc05_fence_after();
 #pragma unroll 1
         for (int cc = 0; cc < D; cc += 32) {
@@ -627,7 +627,7 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         for (int i = 0; i < kC8tBlk; ++i) s[i] *= pow2_whole(fmaxf(r[i / 16], -127.0f));
       }
       uint32_t w[32];
-      if (u >= lb) {  // memory rows: bf16, the tail behind the head
+      if constexpr (kMem) {  // bf16, the tail behind the head
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           w[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
@@ -646,7 +646,13 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       l_run += sum;
       tc05_fence_before();
       mbar_arrive(bar(kCbP0 + 2 * x + (j & 1)));
-    }
+      return true;
+    };
+    const int n_local = max(0, min(u1, lb) - u0);
+    int j = 0;
+    while (j < n_local && block(j, std::false_type{})) ++j;
+    bool okw = j == n_local;
+    while (okw && j < nblk) okw = block(j++, std::true_type{});
     if (okw && nblk > 0) okw = __all_sync(0xffffffffu, wait(kCbO0 + 2 * x + ((nblk - 1) & 1), ((nblk - 1) >> 1) & 1));
     tc05_fence_after();
     const bool have = okw && nblk > 0;
