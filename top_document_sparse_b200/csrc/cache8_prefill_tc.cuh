@@ -154,11 +154,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // grid (pairs * B * H_kv, n_split), block kC8tThreads, one CTA per SM.
-template <int FMT>
+// NG groups of a block's 64 rows have scales of their own: 1 for cache blocks of 64 rows and more, else 4
+// (512 tokens over 8,704 rows in blocks of 64: 116 us with one group, 123 with four).
+template <int FMT, int NG>
 __global__ void __launch_bounds__(kC8tThreads, 1)
 cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
   using Sm = C8tSmem;
-  constexpr int D = 128;
+  constexpr int D = 128, RG = kC8tBlk / NG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -329,9 +331,8 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
     // are loaded a whole block ahead, right after the last ones left their registers.
     const int row0 = 2 * (tid >> 4) + ((tid >> 2) & 1), pc = 4 * ((tid >> 3) & 1) + (tid & 3);
     constexpr int N = kC8tBlk / 16;  // pieces of a half
-    static_assert(N == 4, "a float4 of scales");
     uint4 raw[2][N];
-    float rs[2][N];  // scales of 16 rows each (of the first ones past the last row)
+    float rs[2][NG];  // the groups' scales (the first one's past the last row)
     auto load_raw = [&](int u, int h) {
       if (u >= u1 || u >= lb) return;
       const uint8_t *src = (h ? a.v8 : a.k8) + (bh * a.cap + static_cast<int64_t>(u) * kC8tBlk + row0) * D + 16 * pc;
@@ -341,8 +342,9 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       for (int i = 0; i < N; ++i) {
         raw[h][i] = make_uint4(0, 0, 0, 0);
         if (left >= kC8tBlk || 16 * i + row0 < left) raw[h][i] = ld_stream16(src + 2048 * i);
-        rs[h][i] = __ldg(sc + ((u * kC8tBlk + (16 * i < left ? 16 * i : 0)) >> a.bl_shift));
       }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) rs[h][g] = __ldg(sc + ((u * kC8tBlk + (RG * g < left ? RG * g : 0)) >> a.bl_shift));
     };
     load_raw(u0, 0);
     load_raw(u0, 1);
@@ -352,8 +354,8 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       for (int h = 0; h < 2; ++h) {
         if (!wait_slot(j, h)) continue;
         if (h == 0)
-          put_scales(j, make_float4(rs[0][0], rs[0][1], rs[0][2], rs[0][3]),
-                     make_float4(rs[1][0], rs[1][1], rs[1][2], rs[1][3]), false);
+          put_scales(j, make_float4(rs[0][0], rs[0][1 % NG], rs[0][2 % NG], rs[0][3 % NG]),
+                     make_float4(rs[1][0], rs[1][1 % NG], rs[1][2 % NG], rs[1][3 % NG]), false);
         uint8_t *dst = slot(j, h);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -548,12 +550,20 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
           tmem_st16(at + i, y);
         }
       }
-      const float4 ks = sc[0], rs = sc[1], us = sc[2];
-      // score factors of 16 rows each (positive even where the product underflows, so that a hidden
-      // row stays at -inf)
-      float c[4] = {fmaxf(cf * ks.x, 1.2e-38f), fmaxf(cf * ks.y, 1.2e-38f), fmaxf(cf * ks.z, 1.2e-38f),
-                    fmaxf(cf * ks.w, 1.2e-38f)};
-      const float r[4] = {rs.x, rs.y, rs.z, rs.w};
+      const float4 us = sc[2];
+      // score factors of the groups (positive even where the product underflows, so that a hidden row
+      // stays at -inf) and log2 of V's scales over the unit
+      float c[NG], r[NG];
+      if constexpr (NG == 4) {
+        const float4 ks = sc[0], rs = sc[1];
+        c[0] = ks.x; c[1] = ks.y; c[2] = ks.z; c[3] = ks.w;
+        r[0] = rs.x; r[1] = rs.y; r[2] = rs.z; r[3] = rs.w;
+      } else {
+        c[0] = sc[0].x;
+        r[0] = us.z;
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) c[g] = fmaxf(cf * c[g], 1.2e-38f);
       float alpha = 1.0f;  // factor of O's lane
       if (us.x > 0.0f) {   // a larger unit: the reference falls as in Softmax8
         const float k = reference_falls(m_run, l_run, us.x);
@@ -570,21 +580,27 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
 #pragma unroll
         for (int i = 0; i < kC8tBlk; ++i) s[i] = i < lim ? s[i] : -INFINITY;
       }
-      float top[4], over = -INFINITY;
+      float top[NG], over = -INFINITY;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float mx[2] = {-INFINITY, -INFINITY};
+      for (int g = 0; g < NG; ++g) {
+        constexpr int NA = NG == 1 ? 4 : 2;
+        float mx[NA];
 #pragma unroll
-        for (int i = 16 * g; i < 16 * g + 16; i += 4)
+        for (int e = 0; e < NA; ++e) mx[e] = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
-        top[g] = __fmul_rn(fmaxf(mx[0], mx[1]), c[g]);
+        for (int i = RG * g; i < RG * (g + 1); i += 2 * NA)
+#pragma unroll
+          for (int e = 0; e < NA; ++e) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
+        top[g] = mx[0];
+#pragma unroll
+        for (int e = 1; e < NA; ++e) top[g] = fmaxf(top[g], mx[e]);
+        top[g] = __fmul_rn(top[g], c[g]);
         over = fmaxf(over, top[g] - m_run + fmaxf(r[g], kC8MinRatio));
       }
       if (over > kC8Slack) {
         float m_new = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) m_new = fmaxf(m_new, new_reference(top[g], fmaxf(r[g], kC8MinRatio)));
+        for (int g = 0; g < NG; ++g) m_new = fmaxf(m_new, new_reference(top[g], fmaxf(r[g], kC8MinRatio)));
         const float f = ex2_approx(m_run - m_new);
         m_run = m_new;
         l_run *= f;
@@ -595,8 +611,9 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
         // far scores: the reference came from a rounded product, so the others are rounded alike, and
         // it leaves them before small terms are added that their rounding would swallow
 #pragma unroll
-        for (int i = 0; i < kC8tBlk; ++i) s[i] = __fmul_rn(s[i], c[i / 16]) - ref;
-        c[0] = c[1] = c[2] = c[3] = 1.0f;
+        for (int i = 0; i < kC8tBlk; ++i) s[i] = __fmul_rn(s[i], c[i / RG]) - ref;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) c[g] = 1.0f;
         ref = 0.0f;
       }
       // the ratios of the scales in the exponent, unless they would take weights out of range
@@ -617,21 +634,26 @@ cache8_prefill_tc_kernel(Attend8Args a, int n_pairs) {
       }
       float sum = 0.0f;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < NG; ++g) {
+        constexpr int NA = NG == 1 ? 2 : 1;
         const float rg = fold ? r[g] : 0.0f, mf = ref - kC8Shift - rg;
-        float2 ps = make_float2(0.0f, 0.0f);
+        float2 ps[NA];
 #pragma unroll
-        for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+        for (int e = 0; e < NA; ++e) ps[e] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = RG * g; i < RG * (g + 1); i += 2) {
           const float2 e = fma2(make_float2(s[i], s[i + 1]), make_float2(c[g], c[g]), make_float2(-mf, -mf));
           s[i] = ex2_approx(e.x);
           s[i + 1] = ex2_approx(e.y);
-          ps = add2(ps, make_float2(s[i], s[i + 1]));
+          ps[(i >> 1) % NA] = add2(ps[(i >> 1) % NA], make_float2(s[i], s[i + 1]));
         }
-        sum = fmaf(ps.x + ps.y, pow2_whole(-rg), sum);
+        float own = ps[0].x + ps[0].y;
+        if constexpr (NA == 2) own += ps[1].x + ps[1].y;
+        sum = fmaf(own, pow2_whole(-rg), sum);
       }
       if (!fold) {
 #pragma unroll
-        for (int i = 0; i < kC8tBlk; ++i) s[i] *= pow2_whole(fmaxf(r[i / 16], -127.0f));
+        for (int i = 0; i < kC8tBlk; ++i) s[i] *= pow2_whole(fmaxf(r[i / RG], -127.0f));
       }
       uint32_t w[32];
       if constexpr (kMem) {  // bf16, the tail behind the head

@@ -357,7 +357,7 @@ msa_status attend8_check(const msa_memory *mem, const msa_cache8 *c, int T, int 
 
 template <int FMT>
 msa_status launch_prefill8(const msa::Attend8Args &a, const Attend8Plan &p, int B, cudaStream_t st) {
-  auto kern = msa::cache8_prefill_tc_kernel<FMT>;
+  auto kern = a.bl >= msa::kC8tBlk ? msa::cache8_prefill_tc_kernel<FMT, 1> : msa::cache8_prefill_tc_kernel<FMT, 4>;
   const int smem = msa::C8tSmem::bytes(p.table_cap);
   MSA_CUDA(allow_smem(kern, smem));
   const int64_t ctas = static_cast<int64_t>(B) * a.H_kv * p.col_tiles;
