@@ -511,8 +511,15 @@ MSA_API msa_status msa_sparse_attend_backward(const msa_memory *mem, const void 
  *   factor : >= 1 (not read without a scaling); original_length: >= 1 for YARN
  *   magnitude : 0 takes the scaling's own, 0.1 ln(factor) + 1 for YARN and 1 otherwise
  * head_dim 2..512 and rotary_dim 2..head_dim, both even (NTK: rotary_dim > 2).
- * Frequencies are kept as 64-bit fractions of a turn, so an angle is exact
- * modulo one turn at every int64 position (negative ones too).  The handle is
+ * Frequencies are computed in fp64 and kept as 64-bit fractions of a turn; the
+ * product with any int64 position (negative ones too) is exact modulo one turn
+ * and then rounded to 2^-25 turns.
+ * Retrieved rows: msa_encode_memory rotates the memory's K in one form, whole
+ * heads in half pairs with base rope_theta, unscaled.  A call that attends over
+ * them (k > 0) needs Q and local K in the same form: MSA_ROPE_HALF, rotary_dim
+ * = head_dim, MSA_ROPE_NONE, theta = rope_theta, magnitude 0 or 1.  The other
+ * forms are for k = 0, and for content whose K the caller rotated alike.
+ * The handle is
  * immutable and belongs to the device that was current at its creation, where
  * its calls have to be made; the same holds for a memory in the msa_cache8_* calls.
  */
@@ -603,7 +610,8 @@ typedef struct {
  *              query's tokens are appended, the rest is padding (NULL: all)
  *   start    : device int32 [batch] or NULL: the row the first token goes to;
  *              NULL appends at cache_len[b].  A start below cache_len drops the
- *              rows from there on (rejected draft tokens).  A block that start
+ *              rows from there on (rejected draft tokens); one above it takes the
+ *              rows between as they lie in the buffers.  A block that start
  *              lies in keeps its scale unless start is its first row.
  * cache_len[b] becomes start + n_tokens; weights of appended rows become 0.  Rows that
  * pass the capacity are skipped and flagged (MSA_DEVERR_CACHE_OVERFLOW); a
@@ -650,6 +658,13 @@ MSA_API size_t msa_cache8_attend_workspace_size(const msa_memory *mem, const msa
  *              cached row j, weights[b][g][j] = weight_decay * weights[b][g][j]
  *              + the softmax weight row j received from this call's tokens and
  *              the heads of kv head g (0 overwrites; rows beyond cache_len stay)
+ * Scores, sums and statistics are fp32.  A weight is rounded to 2^-11 (fp32:
+ * 2^-22), and to 2^-28 of the query's largest product of a weight and a V
+ * scale; scales within 2^96 of the largest keep that, whatever weight the
+ * larger ones have.  For the scores, elements of Q below 2^-17 of their head's
+ * largest lose bits (2^-25 of it at most; all of fp32's lose that much), and in
+ * calls of 48 columns (tokens * heads of the group) and more elements of a
+ * retrieved row's K below 2^-10 of the row's largest (2^-19).
  * k may be 0 (content and ids are then not read).  A group
  * (n_q_heads / H_kv) is at most 16.  A count out of [0, tokens] or a length
  * outside [0, capacity] counts as no tokens (MSA_DEVERR_BAD_LENGTH).  O must

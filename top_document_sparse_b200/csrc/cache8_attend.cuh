@@ -19,16 +19,17 @@
 // with the block's scale applied outside: K's to the score; V's to P, as its
 // ratio 2^r to the largest V scale seen so far (the unit), r <= 0.
 // int8 -> fp16 is a byte permute that sets the bits of 1024 + (q + 128) and
-// one subtraction.  Q is scaled by a power of two per column to 1 <= max|q| < 2: elements
-// below 2^-17 of the largest lose bits, 2^-25 of it at most.
-//   P = 2^(s - m + r + 11) in fp16 against a column's reference m, which moves, to
-// 7 to 8 above s + r (log2 units), only when that exceeds it by 4: P is at most 2^15,
-// weights whose product with the scale is down to 2^-17 of the column's largest keep fp16's
-// full 11 bits, smaller ones an error below 2^-28 of that product.  So m follows
-// what a block adds to O, not its scores alone, and when the unit grows m
-// falls by as much, so that O's own unit (m and the unit together) stays: a light block of huge values
-// costs the others nothing.  (With m following the scores, weights behind a block
-// of no weight and 2^24 times larger values kept 3 bits.)  The sum of the weights 2^(s - m) is fp32
+// one subtraction.  Q is scaled by a power of two per column to 1 <= max|q| < 2:
+// elements below 2^-17 of the largest lose bits, 2^-25 of it at most.
+//   P = 2^(s - m + r + 11) in fp16 against a column's reference m, which moves,
+// to 7 to 8 above s + r (log2 units), only when that exceeds it by 4: P is at
+// most 2^15, weights whose product with the scale is down to 2^-17 of the
+// column's largest keep fp16's full 11 bits, smaller ones an error below 2^-28
+// of that product.  So m follows what a block adds to O, not its scores alone,
+// and when the unit grows m falls by as much, so that O's own unit (m and the
+// unit together) stays: a light block of huge values costs the others nothing.
+// (With m following the scores, weights behind a block of no weight and 2^24
+// times larger values kept 3 bits.)  The sum of the weights 2^(s - m) is fp32
 // and takes m's distance from the scores as it is, up to 2^100.
 //   Memory rows are bf16 and go through bf16 MMAs; P is split there into a bf16
 // head and tail, two MMAs, so it loses nothing either.
@@ -375,10 +376,10 @@ struct Softmax8 {
     }
   }
   // s (log2 units, -inf where hidden) of rows whose V scale is 2^r units -> p = 2^(s - m), the sums
-  // and, where s + r passes its column's reference by more than the slack, new references.  The difference comes first and is
-  // compared itself: of scores so large that a unit is below their rounding, s - (m - c) and s > m + c
-  // would be off by that rounding, and p could leave fp16.  (For the same reason a score's product is
-  // rounded by itself, never fused with what is subtracted.)
+  // and, where s + r passes its column's reference by more than the slack, new references.  The
+  // difference comes first and is compared itself: of scores so large that a unit is below their
+  // rounding, s - (m - c) and s > m + c would be off by that rounding, and p could leave fp16.  (For
+  // the same reason a score's product is rounded by itself, never fused with what is subtracted.)
   __device__ __forceinline__ void step(float (&s)[NT][4], float r) {
     const float lim = kC8Slack - r;
     bool over = false;

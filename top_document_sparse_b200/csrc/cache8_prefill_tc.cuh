@@ -9,8 +9,8 @@
 //   converters (warps 10-13) load a block's bytes, widen them to fp16 in
 //        registers and write them to shared memory in the MMA's layout, K and V
 //        each into a ring of four.  Cached values are exact in fp16; their scales
-//        (one for K and one for V of every 16 rows) leave with the block for the
-//        softmax.  K of bf16 memory rows is brought to fp16 by a power of two that
+//        (one for K and one for V, of 16 rows each where cache blocks are that short)
+//        leave with the block for the softmax.  K of bf16 memory rows is brought to fp16 by a power of two that
 //        takes the block's largest element below 2, or, where a row lies 2^6 and more below
 //        another, by one of its own for every row, which leaves with the block (elements
 //        below 2^-10 of their row's largest may lose bits, 2^-19 of it at most).  Their V stays
@@ -28,10 +28,10 @@
 //        a block waits for no P V: the next S is ready when it ends, and only a
 //        move of the reference m (when s + r passes it by 4 in log2 units; to 7 to 8
 //        above) waits for O's last update and rescales O's lane.  r is a whole number
-//        and goes into the exponent; the sum of the weights of 16 rows is brought back by 2^-r.
-// 512 tokens x 32 heads over 8,704 + 128 rows: 166 us with P through shared
-// memory, 153 with blocks of 128 rows and one S a tile (S, softmax and P V of a
-// tile then follow one another).
+//        and goes into the exponent; a group's sum of weights is brought back by 2^-r.
+// 512 tokens x 32 heads over 8,704 + 128 rows: 117 us; before the last steps 166 with
+// P through shared memory against 126, and 153 with blocks of 128 rows and one S a tile
+// (S, softmax and P V of a tile then follow one another).
 // Every wait is bounded: on timeout the CTA raises MSA_DEVERR_WAIT_TIMEOUT,
 // every role skips the rest (the outputs are then void), and issued MMAs are
 // drained before TMEM is freed.

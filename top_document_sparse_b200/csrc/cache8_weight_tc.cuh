@@ -17,7 +17,7 @@
 //   warps 0-7    S from TMEM, the weights added up in registers
 // The special-function unit is the floor: 256 x 128 exponentials take 2,048
 // cycles a scheduler, the MMAs about 1,300; the row warps need 3,970 cycles a
-// tile.  512 tokens x 32 heads over 8,704 rows: 386 us on mma.sync, 94 here;
+// tile.  512 tokens x 32 heads over 8,704 rows: 386 us on mma.sync, 99 here;
 // 718 columns of D = 64 over 16,000 rows 79 against 21.
 // Every wait is bounded as in the attention on tcgen05.
 #pragma once
